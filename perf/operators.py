@@ -286,7 +286,9 @@ def _run_own(s):
     if "ws" not in s:
         s["ws"] = P.Workspace(DEVICE)
     if s["op"] == "clip":
-        norm = P.clip_grad_norm(s["grads"], s["max_norm"], out=s["clipped"], ws=s["ws"])
+        if "list" not in s:  # gradients that stay in place from step to step: laid out once
+            s["list"] = P.GradList(s["grads"], out=s["clipped"])
+        norm = P.clip_grad_norm(s["list"], s["max_norm"], ws=s["ws"])
         return norm, s["buckets"]
     if s["bwd"]:
         return P.gated_ffn_bwd(s["dy"], s["x"], s["wg"], s["wu"], s["wd"], s["g"], s["u"], act=s["act"], ws=s["ws"])
