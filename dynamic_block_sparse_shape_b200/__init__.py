@@ -20,6 +20,7 @@ __all__ = [
     "block_pool", "block_select", "block_select_ex", "select_workspace_size", "topk_from_sparsity",
     "block_audio_bias", "mask_to_csr",
     "bsa_fwd", "bsa_bwd", "check_device_status", "STATUS", "OP", "DEFAULT_CDF_THRESHOLD",
+    "RopeSpec", "rope", "rope_bwd", "GradList", "grad_norm", "scale_grads", "clip_grad_norm",
 ]
 
 DEFAULT_CDF_THRESHOLD = 0.20
@@ -57,6 +58,18 @@ class _ShapeParams(ctypes.Structure):
     _fields_ = [("w_audio", ctypes.c_float), ("gamma", ctypes.c_float), ("gate_max", ctypes.c_float)]
 
 
+class _RopeParams(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("scaling", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis_dim", ctypes.c_int32 * 3), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("trained_len", ctypes.c_double), ("magnitude", ctypes.c_double), ("pos_scale", ctypes.c_double * 3),
+                ("pos_offset", ctypes.c_double * 3)]
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class _SelectParams(ctypes.Structure):
     _fields_ = [("top_k", ctypes.c_int32), ("cdf_threshold", ctypes.c_float),
                 ("head_top_k", ctypes.POINTER(ctypes.c_int32)), ("head_cdf_threshold", ctypes.POINTER(ctypes.c_float)),
@@ -66,6 +79,7 @@ class _SelectParams(ctypes.Structure):
 _P = ctypes.c_void_p
 _I32, _I64, _F32, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _GEO = ctypes.POINTER(_Geometry)
+_DIM3 = ctypes.POINTER(_Dim3)
 
 _SIGNATURES = {
     "prism_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -91,6 +105,12 @@ _SIGNATURES = {
                                      _P, _P, _P, _SZ, _P]),
     "prism_bsa_bwd": (ctypes.c_int, [_GEO, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, _I32, _I32, _I64, _F32,
                                      _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "prism_rope": (ctypes.c_int, [ctypes.POINTER(_RopeParams), _DIM3, _P, _I64, _P, _P, _I32, _I64, _I64, _P, _P, _I32,
+                                  _I64, _I64, ctypes.c_int, _I32, _I32, _P]),
+    "prism_grad_norm": (ctypes.c_int, [_P, _I64, _I32, _P, _P, _SZ, _P]),
+    "prism_grad_norm_workspace_size": (ctypes.c_int, [_I64, ctypes.POINTER(_SZ)]),
+    "prism_grad_scale": (ctypes.c_int, [_P, _I64, _P, _F32, _F32, _P]),
+    "prism_grad_clip": (ctypes.c_int, [_P, _I64, _I32, _F32, _F32, _P, _P, _SZ, _P]),
 }
 
 
@@ -414,6 +434,227 @@ def bsa_bwd(geo: Geometry, zone_shape, q, k, v, o, lse, do, scale, row_ptr, col_
                                _ptr(col_idx), int(nnz), _ptr(dq), _ptr(dk), _ptr(dv), ws.ptr, ws.nbytes,
                                _stream(stream)), "prism_bsa_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------- around the attention
+def _require(ok: bool, what: str, status: int = 1):
+    if not ok:
+        raise PrismError(status, what)
+
+
+class _On:
+    """The device of a call's tensors made current, and the stream it runs on: the one given, or that device's
+    current one. Outputs made on another stream than the call's are recorded on it."""
+
+    def __init__(self, tensors, stream, what):
+        first = tensors[0]
+        index = first.get_device()
+        _require(index >= 0, f"{what}: tensors must be on a CUDA device")
+        for t in tensors:
+            _require(t.get_device() == index, f"{what}: tensors on different devices")
+        self.index, self.given = index, stream
+        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        own = torch.cuda.current_stream(self.index)
+        self.stream = self.given if self.given is not None else own
+        self.foreign = self.given is not None and self.given.cuda_stream != own.cuda_stream
+        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def made(self, *tensors):
+        """Tensors that the call allocated, to be used on its stream."""
+        if self.foreign:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+_ROPE_LAYOUT = {"interleaved": 0, "half": 1}
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class RopeSpec:
+    """The rotation of ``rope``: how many channels of a head each axis rotates and by which angles.
+
+    axis_dims: rotated channels per axis, (t, h, w) of the token grid or one entry for a single position; the channels
+        behind their sum stay as they are. In the Prism models' video towers a 128-wide head has (44, 42, 42).
+    layout: "interleaved" (pair i is channels 2i, 2i + 1) or "half" (i, i + rot_dim / 2).
+    theta: pair j of an axis of n channels turns by theta ** (-2 j / n) per position.
+    scaling, factor, trained_len: "none"; "linear" (frequencies / factor); "ntk" (theta * factor ** (n / (n - 2)));
+        "yarn" (pairs that turn over 32 times in trained_len positions kept, those below once / factor, a ramp between).
+    magnitude: multiplies the rotated channels; None is 1, or 0.1 ln(factor) + 1 with "yarn".
+    pos_scale, pos_offset: per axis, the position p counts as pos_offset + p * pos_scale (for example video frames on
+        the time axis of the audio tokens).
+    """
+
+    def __init__(self, axis_dims, layout="interleaved", theta=10000.0, scaling="none", factor=1.0, trained_len=4096.0,
+                 magnitude=None, pos_scale=None, pos_offset=None):
+        dims = tuple(int(x) for x in axis_dims)
+        _require(len(dims) in (1, 3), "RopeSpec: axis_dims has one or three entries")
+        _require(layout in _ROPE_LAYOUT, f"RopeSpec: layout {layout!r}")
+        _require(scaling in _ROPE_SCALING, f"RopeSpec: scaling {scaling!r}")
+        if magnitude is None:
+            _require(scaling != "yarn" or factor > 0, "RopeSpec: factor must be positive")
+            magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
+        scale = tuple(pos_scale) if pos_scale is not None else (1.0,) * len(dims)
+        offset = tuple(pos_offset) if pos_offset is not None else (0.0,) * len(dims)
+        _require(len(scale) == len(dims) and len(offset) == len(dims), "RopeSpec: one pos_scale and pos_offset per axis")
+        self.axis_dims, self.layout, self.magnitude = dims, layout, float(magnitude)
+        pad = (0,) * (3 - len(dims))
+        self._c = _RopeParams(_ROPE_LAYOUT[layout], _ROPE_SCALING[scaling], len(dims),
+                              (ctypes.c_int32 * 3)(*dims, *pad), float(theta), float(factor), float(trained_len),
+                              float(magnitude), (ctypes.c_double * 3)(*scale, *pad), (ctypes.c_double * 3)(*offset, *pad))
+        self._ref = ctypes.byref(self._c)
+
+
+def _token_stride(t: torch.Tensor, what: str) -> int:
+    """Elements between tokens of a [N, heads, d] tensor with contiguous heads and channels."""
+    _require(t.dim() == 3, f"{what}: [tokens, heads, head_dim] expected")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    _require((d == 1 or sd == 1) and (h == 1 or sh == d), f"{what}: heads and channels must be contiguous")
+    return sn if n > 1 else max(sn, h * d)
+
+
+def _rope(q, k, spec, grid, positions, out, stream, transposed, what):
+    both = (q,) if k is None else (q, k)
+    on = _On(both if positions is None else both + (positions,), stream, what)
+    sq = _token_stride(q, what)
+    n, hq, d = q.shape
+    hk, sk = 0, 0
+    code = _dtype_code(q)
+    if k is not None:
+        sk = _token_stride(k, what)
+        hk = k.shape[1]
+        _require(k.shape[0] == n and k.shape[2] == d, f"{what}: q and k differ in tokens or head_dim")
+        _require(k.dtype == q.dtype, f"{what}: q and k differ in type", 3)
+    if positions is not None:
+        _require(positions.dtype == torch.int32, f"{what}: positions must be int32", 3)
+        _require(positions.numel() == n * len(spec.axis_dims) and positions.is_contiguous(),
+                 f"{what}: positions must be contiguous [tokens, axes]")
+    with on:
+        if out is None:
+            oq = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
+            ok = None if k is None else torch.empty((n, hk, d), dtype=k.dtype, device=k.device)
+            on.made(oq, ok)
+            soq, sok = hq * d, hk * d
+        else:
+            oq, ok = out if k is not None else ((out, None) if torch.is_tensor(out) else (out[0], None))
+            soq = _token_stride(oq, what)
+            sok = 0
+            _require(oq.shape == q.shape and oq.dtype == q.dtype and oq.device == q.device, f"{what}: out is not like q")
+            if k is not None:
+                sok = _token_stride(ok, what)
+                _require(ok.shape == k.shape and ok.dtype == k.dtype and ok.device == k.device,
+                         f"{what}: out is not like k")
+        g = None if grid is None else ctypes.byref(_Dim3(*(int(x) for x in grid)))
+        _check(lib().prism_rope(spec._ref, g, _ptr(positions), n, _ptr(q), _ptr(oq), hq, sq, soq, _ptr(k), _ptr(ok),
+                                hk, sk, sok, code, d, transposed, on.ptr), what)
+    return oq, ok
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], spec: RopeSpec, grid=None,
+         positions: Optional[torch.Tensor] = None, out=None, stream=None):
+    """Rotary positions of Q [N, heads, d] and K [N, heads_k, d] (or None): returns the rotated (q, k).
+
+    grid: the (T, H, W) token grid in raster order, for a three-axis spec; positions: int32 [N, axes] instead of it.
+    With neither, a one-axis spec takes the token's index. out: the pair of tensors to write, (q, k) for in place."""
+    return _rope(q, k, spec, grid, positions, out, stream, 0, "prism_rope")
+
+
+def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], spec: RopeSpec, grid=None,
+             positions: Optional[torch.Tensor] = None, out=None, stream=None):
+    """The gradient of ``rope``: dQ and dK of the rotated tensors (from ``bsa_bwd``) to those of the unrotated ones."""
+    return _rope(dq, dk, spec, grid, positions, out, stream, 1, "prism_rope (transposed)")
+
+
+_NORM = {2: 0, 2.0: 0, "l2": 0, math.inf: 1, "inf": 1}
+
+
+class GradList:
+    """A list of gradients (and where their scaled values go) for ``grad_norm``, ``scale_grads`` and
+    ``clip_grad_norm``, laid out once: a program whose gradients stay in place keeps it from step to step. It holds
+    the tensors, so their memory stays theirs. grads: dense contiguous bf16 / fp32 tensors of one device, any mix; out:
+    None (in place) or one tensor for each, of its size and type."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None):
+        self.grads = list(grads)
+        self.out = None if out is None else list(out)
+        n = len(self.grads)
+        _require(self.out is None or len(self.out) == n, "GradList: as many outputs as gradients")
+        self.device = self.grads[0].device if n else None
+        self._c = (_Tensor * max(n, 1))()
+        for i, t in enumerate(self.grads):
+            _require(t.is_contiguous(), "GradList: gradients must be contiguous")
+            _require(t.device == self.device, "GradList: gradients on different devices")
+            o = None
+            if self.out is not None:
+                o = self.out[i]
+                _require(o.is_contiguous() and o.numel() == t.numel() and o.dtype == t.dtype and
+                         o.device == self.device, "GradList: an output is not like its gradient")
+                o = o.data_ptr()
+            self._c[i] = (t.data_ptr(), o, t.numel(), _dtype_code(t), 0)
+        b = _SZ()
+        _check(lib().prism_grad_norm_workspace_size(n, ctypes.byref(b)), "prism_grad_norm_workspace_size")
+        self.n, self.workspace_bytes = n, int(b.value)
+
+
+def _grad_list(grads, out=None) -> GradList:
+    if isinstance(grads, GradList):
+        _require(out is None, "the GradList has its outputs already")
+        return grads
+    return GradList(grads, out)
+
+
+def _norm_call(grads, ws, device, stream, what):
+    device = grads.device or torch.device(device)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    on = _On(grads.grads[:1] + [norm], stream, what)
+    ws = (ws or Workspace(device)).ensure(grads.workspace_bytes)
+    return norm, on, ws
+
+
+def grad_norm(grads, ord=2, ws: Optional[Workspace] = None, device="cuda", stream=None) -> torch.Tensor:
+    """Global norm (2 or inf) over a list of gradients or a ``GradList``, a device fp32 scalar. ``device`` is read for
+    an empty list only."""
+    grads = _grad_list(grads)
+    _require(ord in _NORM, f"prism_grad_norm: ord {ord!r}")
+    norm, on, ws = _norm_call(grads, ws, device, stream, "prism_grad_norm")
+    with on:
+        on.made(norm, ws.buf)
+        _check(lib().prism_grad_norm(grads._c, grads.n, _NORM[ord], _ptr(norm), ws.ptr, ws.nbytes, on.ptr),
+               "prism_grad_norm")
+    return norm
+
+
+def scale_grads(grads, norm: torch.Tensor, max_norm: float, out=None, eps: float = 1e-6, stream=None):
+    """Multiplies every gradient by min(1, max_norm / (norm + eps)), ``norm`` a device fp32 scalar (for example the
+    root of the sum of ``grad_norm`` squared over the ranks of a sharded layer). In place, or into ``out``."""
+    grads = _grad_list(grads, out)
+    _require(norm.dtype == torch.float32 and norm.numel() == 1, "prism_grad_scale: norm must be one fp32 value", 3)
+    with _On(grads.grads[:1] + [norm], stream, "prism_grad_scale") as on:
+        _check(lib().prism_grad_scale(grads._c, grads.n, _ptr(norm), float(max_norm), float(eps), on.ptr),
+               "prism_grad_scale")
+
+
+def clip_grad_norm(grads, max_norm: float, ord=2, out=None, eps: float = 1e-6, ws: Optional[Workspace] = None,
+                   device="cuda", stream=None) -> torch.Tensor:
+    """``grad_norm`` and ``scale_grads`` of a list of gradients or a ``GradList``: returns the norm before clipping."""
+    grads = _grad_list(grads, out)
+    _require(ord in _NORM, f"prism_grad_clip: ord {ord!r}")
+    norm, on, ws = _norm_call(grads, ws, device, stream, "prism_grad_clip")
+    with on:
+        on.made(norm, ws.buf)
+        _check(lib().prism_grad_clip(grads._c, grads.n, _NORM[ord], float(max_norm), float(eps), _ptr(norm), ws.ptr,
+                                     ws.nbytes, on.ptr), "prism_grad_clip")
+    return norm
 
 
 def default_scale(head_dim: int) -> float:

@@ -1,0 +1,471 @@
+// The global norm of a list of gradients, and their clipping by it: what ends
+// the backward pass of a training step.
+//
+// The mathematics. norm = sqrt(sum over every element of every tensor of g^2)
+// (or the largest |g|), and then g <- g * min(1, max_norm / (norm + eps)).
+//
+// Sums. A thread squares and adds the elements of a few 16-byte vectors in
+// fp32 (kVecs vectors: at most 32 terms in two chains), and adds that to an
+// fp64 sum; a group whose fp32 sum overflowed, or is so small that its squares
+// may have lost bits below the smallest normal number, is squared again in
+// fp64, so gradients of any magnitude that their type holds count in full. The
+// CTAs' sums are written to the workspace and added in a fixed order: no
+// atomics, the same result every time.
+//
+// Work. The tensors are cut into chunks of 16 KB; each CTA takes one contiguous
+// run of chunks, so it looks its tensor up once and then walks on. The table of
+// tensors travels as a kernel parameter (kMany entries per launch), so nothing
+// is copied to the device and a captured graph carries its own table.
+//
+// What bounds it: HBM. The norm reads every element once; the scaling reads and
+// writes each once more, which it has to, since no element may be written
+// before the last one has been read. The scaling pass gives every CTA the same
+// run of chunks and walks it backwards, so that what the norm pass read last
+// (up to the size of L2) is found there.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "host.h"
+
+namespace prism {
+namespace {
+
+constexpr int kGnThreads = 256;
+constexpr int kGnVecs = 4;                                // 16-byte vectors of a thread per chunk
+constexpr int kGnChunkVecs = kGnThreads * kGnVecs;        // 16 KB
+constexpr int kGnCtasPerSm = 6;
+constexpr int kGnMaxCtas = 148 * kGnCtasPerSm;
+constexpr int kMany = 900, kFew = 40;                     // tensors per launch (a kernel takes 32,764 bytes of parameters)
+
+struct GnItem {
+  const char* src;
+  char* dst;
+  int64_t n;       // elements
+  int32_t chunk0;  // first chunk of the launch that is this tensor's
+  int32_t fp32;
+};
+
+template <int CAP>
+struct GnTable {
+  int32_t items, chunks, per_cta;
+  int32_t inf_norm;
+  GnItem item[CAP];
+};
+
+__device__ __forceinline__ bool tiny_or_over(float s) { return !(s > 1e-30f && s < 3e38f); }
+
+// One chunk's part of this thread: kGnVecs vectors of 16 bytes, `at` the
+// address of the first rounded down to 16, the tensor's bytes being [lo, hi).
+template <bool FP32>
+struct Chunk {
+  static constexpr int kE = FP32 ? 4 : 8;
+  uint4 v[kGnVecs];
+
+  static __device__ __forceinline__ void decode(const uint4& u, float* x) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (FP32) {
+        x[i] = __uint_as_float(w[i]);
+      } else {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    }
+  }
+  // Elements outside [lo, hi) count as zero.
+  __device__ __forceinline__ void load(uintptr_t at, uintptr_t lo, uintptr_t hi) {
+#pragma unroll
+    for (int i = 0; i < kGnVecs; ++i) {
+      const uintptr_t a = at + uintptr_t(i) * kGnThreads * 16;
+      if (a >= lo && a + 16 <= hi) {
+        v[i] = *reinterpret_cast<const uint4*>(a);
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (a < hi) {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            const uintptr_t p = a + e * (FP32 ? 4 : 2);
+            if (p >= lo && p < hi) {
+              if constexpr (FP32) w[e] = *reinterpret_cast<const uint32_t*>(p);
+              else w[e >> 1] |= uint32_t(*reinterpret_cast<const uint16_t*>(p)) << ((e & 1) * 16);
+            }
+          }
+        }
+        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  __device__ __forceinline__ double sum_squares() const {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < kGnVecs; ++i) {
+      float x[kE];
+      decode(v[i], x);
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) {
+        s0 = fmaf(x[e], x[e], s0);
+        s1 = fmaf(x[e + 1], x[e + 1], s1);
+      }
+    }
+    const float s = s0 + s1;
+    if (!tiny_or_over(s)) return double(s);
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < kGnVecs; ++i) {
+      float x[kE];
+      decode(v[i], x);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) d = fma(double(x[e]), double(x[e]), d);
+    }
+    return d;
+  }
+  // The bits of the largest magnitude: their order is the values', NaN above infinity.
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kGnVecs; ++i) {
+      float x[kE];
+      decode(v[i], x);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+    }
+    return m;
+  }
+  // The values times f, rounded once, to `delta` bytes further on; whole
+  // vectors where both sides are aligned.
+  __device__ __forceinline__ void store_scaled(float f, uintptr_t at, uintptr_t lo, uintptr_t hi, intptr_t delta) const {
+#pragma unroll
+    for (int i = 0; i < kGnVecs; ++i) {
+      const uintptr_t a = at + uintptr_t(i) * kGnThreads * 16;
+      if (a >= hi) continue;
+      float x[kE];
+      decode(v[i], x);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (FP32) {
+          w[j] = __float_as_uint(x[j] * f);
+        } else {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
+          w[j] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+      }
+      if (a >= lo && a + 16 <= hi && delta % 16 == 0) {
+        *reinterpret_cast<uint4*>(a + delta) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          const uintptr_t p = a + e * (FP32 ? 4 : 2);
+          if (p >= lo && p < hi) {
+            if constexpr (FP32) *reinterpret_cast<uint32_t*>(p + delta) = w[e];
+            else *reinterpret_cast<uint16_t*>(p + delta) = uint16_t(w[e >> 1] >> ((e & 1) * 16));
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int CAP>
+__device__ __forceinline__ int find_item(const GnTable<CAP>& T, int chunk) {
+  int lo = 0, hi = T.items - 1;  // the last item whose first chunk is not behind `chunk`
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (T.item[mid].chunk0 <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Deterministic sum (or maximum) over the CTA; the result is thread 0's.
+__device__ __forceinline__ double cta_reduce(double d, bool maximum) {
+  __shared__ double part[kGnThreads / 32];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const double x = __shfl_down_sync(0xffffffffu, d, o);
+    d = maximum ? (x > d ? x : d) : d + x;
+  }
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = d;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int i = 1; i < kGnThreads / 32; ++i) d = maximum ? (part[i] > d ? part[i] : d) : d + part[i];
+  return d;
+}
+
+// Pass 1: CTA b's run of chunks, [b * per_cta, (b + 1) * per_cta), to
+// partial[b]: a sum of squares, or the largest magnitude's bits as a number.
+template <int CAP>
+__global__ void __launch_bounds__(kGnThreads) norm_kernel(const __grid_constant__ GnTable<CAP> T, double* partial) {
+  int c = blockIdx.x * T.per_cta;
+  const int end = min(c + T.per_cta, T.chunks);
+  double acc = 0.0;
+  uint32_t top = 0;
+  if (c < end) {
+    int it = find_item(T, c);
+    for (; c < end; ++c) {
+      while (it + 1 < T.items && T.item[it + 1].chunk0 <= c) ++it;
+      const GnItem& I = T.item[it];
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(I.src);
+      const uintptr_t at = (lo & ~uintptr_t(15)) + (uintptr_t(c - I.chunk0) * kGnChunkVecs + threadIdx.x) * 16;
+      if (I.fp32) {
+        Chunk<true> k;
+        k.load(at, lo, lo + uintptr_t(I.n) * 4);
+        if (T.inf_norm) top = max(top, k.max_bits());
+        else acc += k.sum_squares();
+      } else {
+        Chunk<false> k;
+        k.load(at, lo, lo + uintptr_t(I.n) * 2);
+        if (T.inf_norm) top = max(top, k.max_bits());
+        else acc += k.sum_squares();
+      }
+    }
+  }
+  const double r = cta_reduce(T.inf_norm ? double(top) : acc, T.inf_norm);
+  if (threadIdx.x == 0) partial[blockIdx.x] = r;
+}
+
+// The norm from every CTA's part, in a fixed order, to every thread of the CTA.
+__device__ __forceinline__ double combine(const double* partial, int parts, bool inf_norm) {
+  __shared__ double norm;
+  double d = 0.0;
+  for (int i = threadIdx.x; i < parts; i += kGnThreads) {
+    const double x = partial[i];
+    d = inf_norm ? (x > d ? x : d) : d + x;
+  }
+  d = cta_reduce(d, inf_norm);
+  if (threadIdx.x == 0) norm = inf_norm ? double(__uint_as_float(uint32_t(d))) : sqrt(d);
+  __syncthreads();
+  return norm;
+}
+
+__global__ void __launch_bounds__(kGnThreads) finish_kernel(const double* partial, int parts, int inf_norm, float* norm) {
+  const double r = combine(partial, parts, inf_norm);
+  if (threadIdx.x == 0) *norm = float(r);
+}
+
+struct GnScale {
+  const double* partial;  // null: the norm is read from `norm`
+  int32_t parts, inf_norm;
+  float* norm;
+  int32_t write_norm;
+  float max_norm, eps;
+};
+
+// Pass 2: the factor, and this CTA's run of chunks times it, last chunk first.
+template <int CAP>
+__global__ void __launch_bounds__(kGnThreads) scale_kernel(const __grid_constant__ GnTable<CAP> T, const GnScale S) {
+  const double norm = S.partial ? combine(S.partial, S.parts, S.inf_norm) : double(*S.norm);
+  if (S.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *S.norm = float(norm);
+  const double f = double(S.max_norm) / (norm + double(S.eps));
+  const float factor = f >= 1.0 ? 1.f : float(f);  // a NaN norm makes every value NaN
+  const int first = blockIdx.x * T.per_cta;
+  int c = min(first + T.per_cta, T.chunks) - 1;
+  if (c < first) return;
+  int it = find_item(T, c);
+  for (; c >= first; --c) {
+    while (T.item[it].chunk0 > c) --it;
+    const GnItem& I = T.item[it];
+    if (factor == 1.f && I.src == I.dst) continue;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(I.src);
+    const uintptr_t at = (lo & ~uintptr_t(15)) + (uintptr_t(c - I.chunk0) * kGnChunkVecs + threadIdx.x) * 16;
+    const intptr_t delta = I.dst - I.src;
+    if (I.fp32) {
+      Chunk<true> k;
+      k.load(at, lo, lo + uintptr_t(I.n) * 4);
+      k.store_scaled(factor, at, lo, lo + uintptr_t(I.n) * 4, delta);
+    } else {
+      Chunk<false> k;
+      k.load(at, lo, lo + uintptr_t(I.n) * 2);
+      k.store_scaled(factor, at, lo, lo + uintptr_t(I.n) * 2, delta);
+    }
+  }
+}
+
+prism_status check_tensors(const prism_tensor* t, int64_t n, bool writes) {
+  if (n < 0 || (n > 0 && !t)) return PRISM_ERR_ARG;
+  if (n > (1 << 20)) return PRISM_ERR_UNSUPPORTED;
+  for (int64_t i = 0; i < n; ++i) {
+    if (t[i].numel < 0) return PRISM_ERR_ARG;
+    if (t[i].dtype != PRISM_BF16 && t[i].dtype != PRISM_FP32) return PRISM_ERR_DTYPE;
+    if (t[i].numel == 0) continue;
+    const uintptr_t es = t[i].dtype == PRISM_FP32 ? 4 : 2;
+    if (!t[i].data || reinterpret_cast<uintptr_t>(t[i].data) % es) return PRISM_ERR_ARG;
+    if (writes && reinterpret_cast<uintptr_t>(t[i].out) % es) return PRISM_ERR_ARG;
+    if (t[i].numel > (int64_t(1) << 43)) return PRISM_ERR_UNSUPPORTED;
+  }
+  return PRISM_OK;
+}
+
+// What one tensor's scaling writes may meet neither another tensor nor, other
+// than exactly, its own input.
+prism_status check_apart(const prism_tensor* t, int64_t n) {
+  struct Range {
+    uintptr_t a, e;
+    bool written;
+  };
+  try {
+    std::vector<Range> r;
+    r.reserve(size_t(n) * 2);
+    for (int64_t i = 0; i < n; ++i) {
+      if (!t[i].numel) continue;
+      const uintptr_t bytes = uintptr_t(t[i].numel) * (t[i].dtype == PRISM_FP32 ? 4 : 2);
+      const uintptr_t s = reinterpret_cast<uintptr_t>(t[i].data);
+      const uintptr_t d = t[i].out ? reinterpret_cast<uintptr_t>(t[i].out) : s;
+      r.push_back({d, d + bytes, true});
+      if (d != s) r.push_back({s, s + bytes, false});
+    }
+    std::sort(r.begin(), r.end(), [](const Range& x, const Range& y) { return x.a < y.a; });
+    uintptr_t end = 0, end_written = 0;  // of the ranges so far
+    for (const Range& x : r) {
+      if (x.a < end_written || (x.written && x.a < end)) return PRISM_ERR_ARG;
+      end = std::max(end, x.e);
+      if (x.written) end_written = std::max(end_written, x.e);
+    }
+  } catch (...) {
+    return PRISM_ERR_UNSUPPORTED;  // no host memory for the check
+  }
+  return PRISM_OK;
+}
+
+// Launches of at most CAP tensors each; F(table, grid, first partial).
+template <int CAP, typename F>
+prism_status each_launch(const prism_tensor* t, int64_t n, bool inf_norm, const F& run) {
+  GnTable<CAP> T;
+  int64_t i = 0;
+  int parts = 0;
+  while (i < n) {
+    T.items = 0;
+    T.inf_norm = inf_norm;
+    int64_t chunks = 0;
+    for (; i < n && T.items < CAP; ++i) {
+      if (!t[i].numel) continue;
+      const int64_t bytes = t[i].numel * (t[i].dtype == PRISM_FP32 ? 4 : 2) +
+                            int64_t(reinterpret_cast<uintptr_t>(t[i].data) % 16);
+      const int64_t c = (bytes + kGnChunkVecs * 16 - 1) / (kGnChunkVecs * 16);
+      if (chunks + c > (int64_t(1) << 30)) {
+        if (T.items == 0) return PRISM_ERR_UNSUPPORTED;
+        break;
+      }
+      GnItem& I = T.item[T.items++];
+      I.src = static_cast<const char*>(t[i].data);
+      I.dst = static_cast<char*>(t[i].out ? t[i].out : t[i].data);
+      I.n = t[i].numel;
+      I.fp32 = t[i].dtype == PRISM_FP32;
+      I.chunk0 = int32_t(chunks);
+      chunks += c;
+    }
+    if (T.items == 0) break;
+    T.chunks = int32_t(chunks);
+    int64_t ctas = std::min<int64_t>(chunks, std::min(device_sm_count() * kGnCtasPerSm, kGnMaxCtas));
+    T.per_cta = int32_t((chunks + ctas - 1) / ctas);
+    ctas = (chunks + T.per_cta - 1) / T.per_cta;
+    const cudaError_t e = run(T, int(ctas), parts);
+    if (e != cudaSuccess) return PRISM_ERR_CUDA;
+    parts += int(ctas);
+  }
+  return PRISM_OK;
+}
+
+size_t norm_ws_bytes(int64_t n) {
+  const int64_t launches = n / kMany + 2;
+  return kWsHeader + align_up(size_t(launches) * kGnMaxCtas * sizeof(double), 256);
+}
+
+prism_status check_norm_ws(void* ws, size_t ws_bytes, int64_t n) {
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 || ws_bytes < norm_ws_bytes(n)) return PRISM_ERR_WORKSPACE;
+  return PRISM_OK;
+}
+
+template <int CAP>
+prism_status run_norm(const prism_tensor* t, int64_t n, bool inf_norm, double* partial, int* parts, cudaStream_t s) {
+  return each_launch<CAP>(t, n, inf_norm, [&](const GnTable<CAP>& T, int ctas, int at) {
+    norm_kernel<CAP><<<ctas, kGnThreads, 0, s>>>(T, partial + at);
+    *parts = at + ctas;
+    return cudaGetLastError();
+  });
+}
+
+template <int CAP>
+prism_status run_scale(const prism_tensor* t, int64_t n, GnScale g, cudaStream_t s) {
+  return each_launch<CAP>(t, n, g.inf_norm, [&](const GnTable<CAP>& T, int ctas, int) {
+    scale_kernel<CAP><<<ctas, kGnThreads, 0, s>>>(T, g);
+    g.write_norm = 0;
+    return cudaGetLastError();
+  });
+}
+
+prism_status norm_parts(const prism_tensor* t, int64_t n, int32_t ord, void* ws, double** partial, int* parts,
+                        cudaStream_t s) {
+  *partial = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) + kWsHeader);
+  *parts = 0;
+  const bool inf_norm = ord == PRISM_NORM_INF;
+  return n <= kFew ? run_norm<kFew>(t, n, inf_norm, *partial, parts, s)
+                   : run_norm<kMany>(t, n, inf_norm, *partial, parts, s);
+}
+
+bool bad_bound(float max_norm, float eps) { return !(max_norm >= 0.f) || !(eps >= 0.f) || std::isinf(eps); }
+
+}  // namespace
+}  // namespace prism
+
+using namespace prism;
+
+extern "C" prism_status prism_grad_norm_workspace_size(int64_t n_tensors, size_t* bytes) {
+  if (!bytes || n_tensors < 0) return PRISM_ERR_ARG;
+  if (n_tensors > (1 << 20)) return PRISM_ERR_UNSUPPORTED;
+  *bytes = norm_ws_bytes(n_tensors);
+  return PRISM_OK;
+}
+
+extern "C" prism_status prism_grad_norm(const prism_tensor* grads, int64_t n_tensors, int32_t ord, float* norm,
+                                        void* ws, size_t ws_bytes, void* stream) {
+  if (!norm || reinterpret_cast<uintptr_t>(norm) % 4) return PRISM_ERR_ARG;
+  if (ord != PRISM_NORM_L2 && ord != PRISM_NORM_INF) return PRISM_ERR_ARG;
+  prism_status st = check_tensors(grads, n_tensors, false);
+  if (st == PRISM_OK) st = check_norm_ws(ws, ws_bytes, n_tensors);
+  if (st != PRISM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  double* partial;
+  int parts;
+  st = norm_parts(grads, n_tensors, ord, ws, &partial, &parts, s);
+  if (st != PRISM_OK) return st;
+  finish_kernel<<<1, kGnThreads, 0, s>>>(partial, parts, ord == PRISM_NORM_INF, norm);
+  return cuda_status(cudaGetLastError());
+}
+
+extern "C" prism_status prism_grad_scale(const prism_tensor* grads, int64_t n_tensors, const float* norm,
+                                         float max_norm, float eps, void* stream) {
+  if (!norm || reinterpret_cast<uintptr_t>(norm) % 4 || bad_bound(max_norm, eps)) return PRISM_ERR_ARG;
+  prism_status st = check_tensors(grads, n_tensors, true);
+  if (st == PRISM_OK) st = check_apart(grads, n_tensors);
+  if (st != PRISM_OK) return st;
+  GnScale g = {nullptr, 0, 0, const_cast<float*>(norm), 0, max_norm, eps};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return n_tensors <= kFew ? run_scale<kFew>(grads, n_tensors, g, s) : run_scale<kMany>(grads, n_tensors, g, s);
+}
+
+extern "C" prism_status prism_grad_clip(const prism_tensor* grads, int64_t n_tensors, int32_t ord, float max_norm,
+                                        float eps, float* norm, void* ws, size_t ws_bytes, void* stream) {
+  if (!norm || reinterpret_cast<uintptr_t>(norm) % 4 || bad_bound(max_norm, eps)) return PRISM_ERR_ARG;
+  if (ord != PRISM_NORM_L2 && ord != PRISM_NORM_INF) return PRISM_ERR_ARG;
+  prism_status st = check_tensors(grads, n_tensors, true);
+  if (st == PRISM_OK) st = check_norm_ws(ws, ws_bytes, n_tensors);
+  if (st == PRISM_OK) st = check_apart(grads, n_tensors);
+  if (st != PRISM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  double* partial;
+  int parts;
+  st = norm_parts(grads, n_tensors, ord, ws, &partial, &parts, s);
+  if (st != PRISM_OK) return st;
+  if (parts == 0) {  // nothing but empty tensors
+    finish_kernel<<<1, kGnThreads, 0, s>>>(partial, 0, ord == PRISM_NORM_INF, norm);
+    return cuda_status(cudaGetLastError());
+  }
+  GnScale g = {partial, parts, ord == PRISM_NORM_INF, norm, 1, max_norm, eps};
+  return n_tensors <= kFew ? run_scale<kFew>(grads, n_tensors, g, s) : run_scale<kMany>(grads, n_tensors, g, s);
+}

@@ -415,6 +415,127 @@ PRISM_API prism_status prism_bsa_bwd(const prism_geometry* geo, const int32_t* z
                            const int32_t* col_idx, int64_t nnz, void* dq, void* dk, void* dv, void* ws,
                            size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the attention in one layer's training step: the
+ * rotation of Q and K before it, the feed-forward block after it, and the
+ * clipping of the gradients that the backward passes leave.
+ * ---------------------------------------------------------------------- */
+
+/* Which channels of a head form pair i of its rot_dim rotated channels. */
+typedef enum {
+  PRISM_ROPE_INTERLEAVED = 0, /* 2i and 2i + 1 */
+  PRISM_ROPE_HALF = 1         /* i and i + rot_dim / 2 */
+} prism_rope_layout;
+
+/* How the frequencies are stretched for contexts longer than those trained. */
+typedef enum {
+  PRISM_ROPE_UNSCALED = 0,
+  PRISM_ROPE_LINEAR = 1, /* every frequency divided by factor */
+  PRISM_ROPE_NTK = 2,    /* theta * factor^(n / (n - 2)), n the axis's channels */
+  PRISM_ROPE_YARN = 3    /* per pair: kept, divided by factor, or a share of both */
+} prism_rope_scaling;
+
+/*
+ * The rotation. The first rot_dim = sum of axis_dim channels of a head are
+ * rotated, in pairs: those of axis 0 first, then axis 1, then axis 2 (in the
+ * half layout the pairs are numbered over the whole rotated part, so an axis
+ * owns one run of channels in either half). Pair j of an axis of n channels
+ * has the frequency theta^(-2j/n), stretched as `scaling` says; the token at
+ * position p of that axis turns by (pos_offset + p * pos_scale) * frequency.
+ * With PRISM_ROPE_YARN a pair that turns more than 32 times over trained_len
+ * positions keeps its frequency, one that turns less than once has it divided
+ * by factor, and a linear ramp over the pair's index lies between the two
+ * (from floor to ceil of the border indices).
+ */
+typedef struct {
+  int32_t layout;      /* prism_rope_layout */
+  int32_t scaling;     /* prism_rope_scaling */
+  int32_t n_axes;      /* 3: (t, h, w) of the token grid; 1: one position */
+  int32_t axis_dim[3]; /* rotated channels of each axis, even, >= 0; their sum in 2..head_dim */
+  double theta;        /* > 1 */
+  double factor;       /* > 0, read unless PRISM_ROPE_UNSCALED */
+  double trained_len;  /* > 0, read with PRISM_ROPE_YARN */
+  double magnitude;    /* every rotated channel is multiplied by it (1: a pure rotation) */
+  double pos_scale[3], pos_offset[3];
+} prism_rope_params;
+
+/*
+ * Rotary positions of q and, unless k is NULL, of k.
+ *
+ * Pair (x1, x2) at angle a becomes m (x1 cos a - x2 sin a), m (x2 cos a + x1
+ * sin a); with `transposed` the angle is -a, which is the gradient of the
+ * rotation: pass dQ and dK of prism_bsa_bwd. Channels behind rot_dim keep
+ * their bits. Angles are formed in 64 bits, the products in 32, and each
+ * output is rounded once.
+ *
+ * positions: device int32 [n_tokens, n_axes], any values; NULL takes the
+ *       raster order: (t, h, w) of `grid` with n_axes 3 (t * h * w ==
+ *       n_tokens, PRISM_ERR_SHAPE otherwise), the token's index with 1.
+ * grid: host, read only for that; may be NULL otherwise.
+ * n_tokens: 0 .. 2^30; 0 does nothing.
+ * q: device [n_tokens, heads_q, head_dim], k: [n_tokens, heads_k, head_dim]
+ *       (heads_k may differ: grouped heads), bf16 or fp32, contiguous heads
+ *       and channels, token strides in elements at least heads * head_dim and
+ *       at most 2^31. head_dim is even and at most 256. Any address and stride of whole
+ *       elements is taken; 16-byte alignment is fastest.
+ * q_out, k_out: device outs of the same dtype, with strides of their own. An
+ *       output may be exactly its input (in place); otherwise no output may
+ *       share memory with another tensor of the call (PRISM_ERR_ARG; views of
+ *       one packed buffer with equal strides are told apart).
+ * No workspace.
+ */
+PRISM_API prism_status prism_rope(const prism_rope_params* params, const prism_dim3* grid, const int32_t* positions,
+                                  int64_t n_tokens, const void* q, void* q_out, int32_t heads_q, int64_t q_stride,
+                                  int64_t q_out_stride, const void* k, void* k_out, int32_t heads_k,
+                                  int64_t k_stride, int64_t k_out_stride, prism_dtype dtype, int32_t head_dim,
+                                  int32_t transposed, void* stream);
+
+typedef enum { PRISM_NORM_L2 = 0, PRISM_NORM_INF = 1 } prism_norm_order;
+
+/* One gradient of a list. */
+typedef struct {
+  void* data;     /* device, numel contiguous values; NULL allowed when numel is 0 */
+  void* out;      /* where its scaled values go; NULL: in place. Not read by prism_grad_norm */
+  int64_t numel;  /* >= 0 */
+  int32_t dtype;  /* prism_dtype, of data and out */
+  int32_t reserved;
+} prism_tensor;
+
+/*
+ * Global norm over every value of a list of tensors (types may be mixed):
+ * norm = sqrt(sum g^2), or the largest |g| with PRISM_NORM_INF. Sums are kept
+ * in fp64 and added in a fixed order (the same bits every time for the same
+ * list on the same GPU model). A NaN or infinite value shows in the norm; an
+ * empty list has norm 0.
+ *
+ * grads: host array of n_tensors (0 .. 2^20) entries; a tensor listed twice
+ *       counts twice. norm: device float out.
+ * ws: at least prism_grad_norm_workspace_size(n_tensors) bytes.
+ * A step whose gradients are split over ranks (a layer sharded by heads) adds
+ * up norm^2 over the ranks between prism_grad_norm and prism_grad_scale.
+ */
+PRISM_API prism_status prism_grad_norm(const prism_tensor* grads, int64_t n_tensors, int32_t ord, float* norm,
+                                       void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of prism_grad_norm and prism_grad_clip. Host only. */
+PRISM_API prism_status prism_grad_norm_workspace_size(int64_t n_tensors, size_t* bytes);
+
+/*
+ * Scales every value by min(1, max_norm / (norm + eps)) with the norm read
+ * from device memory (rounded once to its type). A factor of 1 leaves in-place
+ * tensors untouched; a NaN norm makes every value NaN, an infinite one makes
+ * finite values 0. max_norm >= 0 (infinity: no clipping); eps >= 0.
+ * No tensor's output may share memory with another tensor of the list or, other
+ * than exactly, with its own input (PRISM_ERR_ARG).
+ */
+PRISM_API prism_status prism_grad_scale(const prism_tensor* grads, int64_t n_tensors, const float* norm,
+                                        float max_norm, float eps, void* stream);
+
+/* prism_grad_norm followed by prism_grad_scale with that norm, in fewer
+ * launches and with the factor from the unrounded fp64 norm. */
+PRISM_API prism_status prism_grad_clip(const prism_tensor* grads, int64_t n_tensors, int32_t ord, float max_norm,
+                                       float eps, float* norm, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
