@@ -20,7 +20,7 @@ __all__ = [
     "block_pool", "block_select", "block_select_ex", "select_workspace_size", "topk_from_sparsity",
     "block_audio_bias", "mask_to_csr",
     "bsa_fwd", "bsa_bwd", "check_device_status", "STATUS", "OP", "DEFAULT_CDF_THRESHOLD",
-    "RopeSpec", "rope", "rope_bwd", "GradList", "grad_norm", "scale_grads", "clip_grad_norm",
+    "RopeSpec", "rope", "rope_bwd", "gated_ffn_fwd", "gated_ffn_bwd", "GradList", "grad_norm", "scale_grads", "clip_grad_norm",
 ]
 
 DEFAULT_CDF_THRESHOLD = 0.20
@@ -70,6 +70,12 @@ class _Tensor(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class _FfnWeights(ctypes.Structure):
+    _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("up_stride", ctypes.c_int64), ("down_stride", ctypes.c_int64),
+                ("d", ctypes.c_int32), ("f", ctypes.c_int32)]
+
+
 class _SelectParams(ctypes.Structure):
     _fields_ = [("top_k", ctypes.c_int32), ("cdf_threshold", ctypes.c_float),
                 ("head_top_k", ctypes.POINTER(ctypes.c_int32)), ("head_cdf_threshold", ctypes.POINTER(ctypes.c_float)),
@@ -107,6 +113,11 @@ _SIGNATURES = {
                                      _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
     "prism_rope": (ctypes.c_int, [ctypes.POINTER(_RopeParams), _DIM3, _P, _I64, _P, _P, _I32, _I64, _I64, _P, _P, _I32,
                                   _I64, _I64, ctypes.c_int, _I32, _I32, _P]),
+    "prism_gated_ffn_fwd": (ctypes.c_int, [ctypes.POINTER(_FfnWeights), _I64, _I32, ctypes.c_int, _P, _I64, _P, _I64, _P,
+                                           _P, _P, _SZ, _P]),
+    "prism_gated_ffn_bwd": (ctypes.c_int, [ctypes.POINTER(_FfnWeights), _I64, _I32, ctypes.c_int, _P, _I64, _P, _I64, _P,
+                                           _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "prism_gated_ffn_workspace_size": (ctypes.c_int, [_I64, _I32, _I32, ctypes.POINTER(_SZ)]),
     "prism_grad_norm": (ctypes.c_int, [_P, _I64, _I32, _P, _P, _SZ, _P]),
     "prism_grad_norm_workspace_size": (ctypes.c_int, [_I64, ctypes.POINTER(_SZ)]),
     "prism_grad_scale": (ctypes.c_int, [_P, _I64, _P, _F32, _F32, _P]),
@@ -573,6 +584,86 @@ def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], spec: RopeSpec, grid=
              positions: Optional[torch.Tensor] = None, out=None, stream=None):
     """The gradient of ``rope``: dQ and dK of the rotated tensors (from ``bsa_bwd``) to those of the unrotated ones."""
     return _rope(dq, dk, spec, grid, positions, out, stream, 1, "prism_rope (transposed)")
+
+
+_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+
+
+def _row_stride(t: torch.Tensor, shape, what: str) -> int:
+    """Elements between the rows of a matrix of the given shape with contiguous rows."""
+    _require(t.dim() == 2 and (shape is None or tuple(t.shape) == shape), f"{what} must be {list(shape or 'mn')}")
+    _require(t.shape[1] == 1 or t.stride(1) == 1, f"{what}: rows must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), -(-t.shape[1] // 8) * 8)
+
+
+def _ffn_weights(w_gate, w_up, w_down, what):
+    _require(w_gate.dim() == 2, f"{what}: w_gate must be [f, d]")
+    f, d = w_gate.shape
+    sg, su = _row_stride(w_gate, None, f"{what}: w_gate"), _row_stride(w_up, (f, d), f"{what}: w_up")
+    sd = _row_stride(w_down, (d, f), f"{what}: w_down")
+    return _FfnWeights(w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), sg, su, sd, d, f), d, f
+
+
+def _ffn_workspace(ws, m, f, backward, device):
+    b = _SZ()
+    _check(lib().prism_gated_ffn_workspace_size(m, f, backward, ctypes.byref(b)), "prism_gated_ffn_workspace_size")
+    return (ws or Workspace(device, b.value)).ensure(b.value)
+
+
+def _same_type(tensors, what):
+    for t in tensors:
+        _require(t.dtype == tensors[0].dtype, f"{what}: tensors of different types", 3)
+    return _dtype_code(tensors[0])
+
+
+def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, act: str = "silu",
+                  save: bool = True, out: Optional[torch.Tensor] = None, ws: Optional[Workspace] = None, stream=None):
+    """Gated feed-forward block y = (act(x Wg^T) * (x Wu^T)) Wd^T of x [m, d], weights Wg, Wu [f, d], Wd [d, f] (bf16).
+
+    act: "silu", "gelu", "gelu_tanh" or "relu". Returns (y, gate, up): with ``save`` the projections [m, f] that
+    ``gated_ffn_bwd`` needs, else None. out: where y goes."""
+    what = "prism_gated_ffn_fwd"
+    _require(act in _ACT, f"{what}: act {act!r}")
+    code = _same_type((x, w_gate, w_up, w_down) + (() if out is None else (out,)), what)
+    w, d, f = _ffn_weights(w_gate, w_up, w_down, what)
+    sx = _row_stride(x, (x.shape[0], d), f"{what}: x")
+    m = x.shape[0]
+    with _On((x, w_gate, w_up, w_down) + (() if out is None else (out,)), stream, what) as on:
+        ws = _ffn_workspace(ws, m, f, 0, x.device)
+        y = torch.empty((m, d), dtype=x.dtype, device=x.device) if out is None else out
+        gate = torch.empty((m, f), dtype=x.dtype, device=x.device) if save else None
+        up = torch.empty((m, f), dtype=x.dtype, device=x.device) if save else None
+        on.made(y, gate, up, ws.buf)
+        _check(lib().prism_gated_ffn_fwd(ctypes.byref(w), m, _ACT[act], code, _ptr(x), sx, _ptr(y),
+                                         _row_stride(y, (m, d), f"{what}: out"), _ptr(gate), _ptr(up), ws.ptr,
+                                         ws.nbytes, on.ptr), what)
+    return y, gate, up
+
+
+def gated_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+                  gate: torch.Tensor, up: torch.Tensor, act: str = "silu", need_dx: bool = True, need_dw: bool = True,
+                  ws: Optional[Workspace] = None, stream=None):
+    """Gradient of ``gated_ffn_fwd`` at its saved projections: (dx, dw_gate, dw_up, dw_down); without ``need_dx`` or
+    ``need_dw`` None in their places."""
+    what = "prism_gated_ffn_bwd"
+    _require(act in _ACT, f"{what}: act {act!r}")
+    every = (dy, x, w_gate, w_up, w_down, gate, up)
+    code = _same_type(every, what)
+    w, d, f = _ffn_weights(w_gate, w_up, w_down, what)
+    m = x.shape[0]
+    sx, sdy = _row_stride(x, (m, d), f"{what}: x"), _row_stride(dy, (m, d), f"{what}: dy")
+    for t in (gate, up):
+        _require(tuple(t.shape) == (m, f) and t.is_contiguous(), f"{what}: gate and up must be contiguous [m, f]")
+    with _On(every, stream, what) as on:
+        ws = _ffn_workspace(ws, m, f, 1, x.device)
+        new = lambda *s: torch.empty(s, dtype=x.dtype, device=x.device)  # noqa: E731
+        dx = new(m, d) if need_dx else None
+        dwg, dwu, dwd = (new(f, d), new(f, d), new(d, f)) if need_dw else (None, None, None)
+        on.made(dx, dwg, dwu, dwd, ws.buf)
+        _check(lib().prism_gated_ffn_bwd(ctypes.byref(w), m, _ACT[act], code, _ptr(dy), sdy, _ptr(x), sx, _ptr(gate),
+                                         _ptr(up), _ptr(dx), d, _ptr(dwg), _ptr(dwu), _ptr(dwd), ws.ptr, ws.nbytes,
+                                         on.ptr), what)
+    return dx, dwg, dwu, dwd
 
 
 _NORM = {2: 0, 2.0: 0, "l2": 0, math.inf: 1, "inf": 1}

@@ -1,0 +1,16 @@
+// The products of the feed-forward block, one call per kind (gated_ffn.cu
+// puts them together; each kind is a source file of its own, so they compile
+// side by side).
+#pragma once
+#include "gemm_host.cuh"
+
+namespace prism {
+// h = act(x Wg^T) (x Wu^T), with `save` also both projections
+prism_status ffn_gate_product(int act, GemmArgs& P, const GemmProblem& pr, cudaStream_t s);
+// dh = dy Wd and from it dg, du, with `save` also h
+prism_status ffn_gate_bwd_product(int act, GemmArgs& P, const GemmProblem& pr, cudaStream_t s);
+// both operands K-major / B MN-major / both MN-major
+prism_status ffn_product_nt(GemmArgs& P, const GemmProblem& pr, cudaStream_t s);
+prism_status ffn_product_nn(GemmArgs& P, const GemmProblem& pr, cudaStream_t s);
+prism_status ffn_products_tn(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s);
+}  // namespace prism

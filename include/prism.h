@@ -536,6 +536,62 @@ PRISM_API prism_status prism_grad_scale(const prism_tensor* grads, int64_t n_ten
 PRISM_API prism_status prism_grad_clip(const prism_tensor* grads, int64_t n_tensors, int32_t ord, float max_norm,
                                        float eps, float* norm, void* ws, size_t ws_bytes, void* stream);
 
+typedef enum {
+  PRISM_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+  PRISM_ACT_GELU = 1,      /* g Phi(g) */
+  PRISM_ACT_GELU_TANH = 2, /* 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
+  PRISM_ACT_RELU = 3
+} prism_activation;
+
+/* The weights of a gated feed-forward block of model width d and inner width
+ * f: device bf16 w_gate, w_up [f, d] and w_down [d, f], each with a row stride
+ * in elements (w_gate and w_up may be the halves of one [2 f, d] matrix). */
+typedef struct {
+  const void *w_gate, *w_up, *w_down;
+  int64_t gate_stride, up_stride, down_stride;
+  int32_t d, f;
+} prism_ffn_weights;
+
+/*
+ * Gated feed-forward block: y = (act(x w_gate^T) * (x w_up^T)) w_down^T.
+ *
+ * m tokens (0 .. 2^30; 0 does nothing); d and f multiples of 8, at most 2^20
+ *       (PRISM_ERR_UNSUPPORTED otherwise); bf16 only (PRISM_ERR_DTYPE). Every
+ *       pointer is 16-byte aligned and every row stride a multiple of 8
+ *       elements, at least its row's width and below 2^31.
+ * x, y: device [m, d].
+ * gate, up: device [m, f] contiguous outs, or both NULL: the projections
+ *       x w_gate^T and x w_up^T, rounded, for the backward pass.
+ * Products accumulate in fp32; h = act(gate) * up is formed from the unrounded
+ * projections and rounded to bf16 once, as an operand of the second product.
+ * No output may share memory with gate, up or the weights; y may be x.
+ * ws: at least prism_gated_ffn_workspace_size(m, f, 0) bytes (the status word
+ *       and h).
+ */
+PRISM_API prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t m, int32_t act, prism_dtype dtype,
+                                           const void* x, int64_t x_stride, void* y, int64_t y_stride, void* gate,
+                                           void* up, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of prism_gated_ffn_fwd at the saved projections gate, up [m, f]
+ * (contiguous): with dh = dy w_down, dg = dh up act'(gate), du = dh act(gate)
+ * (each rounded to bf16 once): dx = dg w_gate + du w_up, dw_gate = dg^T x,
+ * dw_up = du^T x, dw_down = dy^T (act(gate) up). relu'(0) = 0.
+ * dx: device [m, d] out, or NULL. dw_gate, dw_up [f, d], dw_down [d, f]: device
+ *       contiguous outs, or all NULL (frozen weights). m = 0 zeroes them.
+ * No output may share memory with any other tensor of the call.
+ * ws: at least prism_gated_ffn_workspace_size(m, f, 1) bytes (the status word,
+ *       dg, du and act(gate) up).
+ */
+PRISM_API prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t m, int32_t act, prism_dtype dtype,
+                                           const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                           const void* gate, const void* up, void* dx, int64_t dx_stride,
+                                           void* dw_gate, void* dw_up, void* dw_down, void* ws, size_t ws_bytes,
+                                           void* stream);
+
+/* Workspace bytes of prism_gated_ffn_fwd (backward 0) and _bwd (1). Host only. */
+PRISM_API prism_status prism_gated_ffn_workspace_size(int64_t m, int32_t f, int32_t backward, size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif
