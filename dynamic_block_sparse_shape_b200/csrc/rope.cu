@@ -7,21 +7,31 @@
 //   a = (offset_x + p_x * scale_x) * f_i
 // of its axis x (t, h, w of the token grid, or one given position):
 //   y1 = m (x1 cos a - x2 sin a),  y2 = m (x2 cos a + x1 sin a).
-// The transposed rotation (the gradient) is the same with -a. The frequencies
-// f_i come from the host in 64 bits as turns per position (f_i / 2 pi), so a
-// position anywhere in the int32 range keeps its fraction of a turn: the turn
-// is one fp64 multiply-add, reduced to [-1/2, 1/2] in fp64, and only then
-// rounded to fp32 (an error of 2^-25 turns at most) for sin and cos.
+// The transposed rotation (the gradient) is the same with -a. Only the
+// fraction of a turn matters, so a / 2 pi is formed modulo 1 as a 64-bit fixed
+// point number: the host gives scale f / 2 pi and offset f / 2 pi as fractions
+// of 2^64 (from fp64), the kernel multiplies the first by the position and
+// adds the second with wrap-around, exact for every int32 position. Its top 32
+// bits become fp32 (off by 2^-26 turns at most) for sin and cos.
 //
 // What bounds it: HBM, every element read once and written once, three
 // operations each. The angles depend on (token, pair) alone, so a CTA computes
-// those of its few tokens once into shared memory (two values per pair) and
-// every head of Q and K reads them from there; a thread keeps one vector's
-// place inside the head and walks the heads, so its cosines and sines sit in
-// registers per token and the loop has no divisions. kBatch vectors per thread
-// are in flight before the first is used.
+// those of its few tokens once into shared memory and every head of Q and K
+// reads them from there. A thread keeps one vector's place inside the head and
+// walks the heads, so its cosines and sines sit in registers per token. All of
+// a CTA's vectors are copied to shared memory asynchronously before the angles
+// are computed (each thread reads back what it copied itself): 24 KB in flight
+// per CTA and no registers held, where loads into registers left the kernel
+// waiting on them. Q and K of the 2K grid (7.25 GB moved): 1.04 ms, 6.97 TB/s
+// (the register version: 1.18 ms; flattening heads and tokens into one list of
+// work cost 1.8 ms in index arithmetic).
+//
+// The half layout with a half that is no multiple of 16 bytes goes through
+// rope_staged_kernel: whole rows in 16-byte vectors to shared memory, rotated
+// there in place by narrower vectors, and back in 16-byte vectors.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -33,8 +43,24 @@ namespace {
 constexpr int kRopeMaxHeadDim = 256;
 constexpr int kRopeMaxPairs = kRopeMaxHeadDim / 2;
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTokens = 8;  // tokens per CTA
-constexpr int kBatch = 4;
+constexpr int kRopeMaxTokens = 16;       // of a CTA
+constexpr int kRopeSmem = 24 * 1024;     // a CTA's vectors in flight
+constexpr int kRopeMaxHeadGroups = 12;   // heads side by side: several heads per thread share its cosines and sines
+
+
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery,
+// "Division by invariant integers using multiplication").
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  return {d, uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1), l};
+}
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const FastDiv& f) {
+  return uint32_t((uint64_t(__umulhi(n, f.mul)) + n) >> f.shift);
+}
 
 struct RopeArgs {
   const void* src[2];  // Q, K
@@ -42,16 +68,17 @@ struct RopeArgs {
   int64_t src_ld[2], dst_ld[2];  // elements between tokens
   int64_t n;                     // tokens
   const int32_t* pos;            // [n, axes], or null: the raster grid
-  int heads_q, heads;            // heads of Q, of both
+  int heads[2];
   int head_dim, pairs;
   int axes;          // 1 or 3
   int pair1, pair2;  // first pair of axis 1, of axis 2
-  int grid_h, grid_w;
+  FastDiv by_w, by_h, by_pairs;
   int rot_units, units;  // vectors (half: vector pairs) a head's rotated part has, and all that are touched
   int head_groups, token_groups, tokens;  // of a CTA
+  int vec_offset;        // of the vectors in shared memory
   float m, sign;
-  double turn[kRopeMaxPairs];   // turns per position
-  double start[kRopeMaxPairs];  // turns at position 0
+  uint64_t turn[kRopeMaxPairs];   // turns per position, modulo 1, in 2^-64
+  uint64_t start[kRopeMaxPairs];  // turns at position 0
 };
 
 // EV elements at an address aligned to their size.
@@ -73,109 +100,199 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// The rotated pair, its roundings spelt out: every variant gives the same bits.
+__device__ __forceinline__ float turn1(float x1, float x2, float c, float s) { return fmaf(x1, c, -__fmul_rn(x2, s)); }
+__device__ __forceinline__ float turn2(float x1, float x2, float c, float s) { return fmaf(x2, c, __fmul_rn(x1, s)); }
+
+// BYTES (4, 8 or 16, aligned) from global to shared memory without a register.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+
+// m cos a and m sin a (signed) of the CTA's tokens n0 .. n0 + end - 1, all pairs.
+__device__ __forceinline__ void rope_angles(const RopeArgs& P, int64_t n0, int end, float* cosines, float* sines) {
+  for (int x = threadIdx.x; x < end * P.pairs; x += blockDim.x) {
+    const int tok = quotient(x, P.by_pairs), i = x - tok * P.pairs;
+    const int64_t n = n0 + tok;
+    const int axis = i < P.pair1 ? 0 : i < P.pair2 ? 1 : 2;
+    int p = int(n);
+    if (P.pos) {
+      p = P.pos[n * P.axes + axis];
+    } else if (P.axes == 3) {
+      const uint32_t row = quotient(uint32_t(n), P.by_w), t = quotient(row, P.by_h);
+      p = axis == 2 ? int(uint32_t(n) - row * P.by_w.d) : axis == 1 ? int(row - t * P.by_h.d) : int(t);
+    }
+    const uint64_t turns = uint64_t(int64_t(p)) * P.turn[i] + P.start[i];
+    float s, c;
+    sincospif(float(int32_t(turns >> 32)) * (1.f / 2147483648.f), &s, &c);
+    cosines[x] = c * P.m;
+    sines[x] = s * P.m * P.sign;
+  }
+}
+
 // HALF: a unit is two vectors of EV elements, rot/2 apart; otherwise one
 // vector of EV elements, EV/2 pairs. EV is the widest vector that the sizes,
 // strides and addresses allow (16 bytes on every usual layout). With ELEM the
 // vector's elements are loaded and stored one by one (an interleaved pair at
-// an address that is no multiple of its size).
-template <typename T, int EV, bool HALF, bool ELEM>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs P) {
-  extern __shared__ float2 cs[];  // [tokens][pairs]: m cos a, m sin a
+// an address that is no multiple of its size). MIXED: an interleaved vector
+// may hold unrotated pairs; it is computed like the others, and they are kept.
+template <typename T, int EV, bool HALF, bool ELEM, bool MIXED, bool ASYNC>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeArgs P) {
+  constexpr int kPairs = HALF ? EV : EV / 2;  // of a unit
+  constexpr int kVecs = HALF ? 2 : 1;
+  using V = Vec<T, EV>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* const cosines = reinterpret_cast<float*>(smem);  // [tokens][pairs]: m cos a, then m sin a
+  float* const sines = cosines + P.tokens * P.pairs;
+  V* const mine = reinterpret_cast<V*>(smem + P.vec_offset) + threadIdx.x;  // every blockDim.x-th is this thread's
   const int64_t n0 = int64_t(blockIdx.x) * P.tokens;
-  for (int x = threadIdx.x; x < P.tokens * P.pairs; x += blockDim.x) {
-    const int tok = x / P.pairs, i = x - tok * P.pairs;
-    const int64_t n = n0 + tok;
-    if (n >= P.n) break;
-    const int axis = i < P.pair1 ? 0 : i < P.pair2 ? 1 : 2;
-    int p;
-    if (P.pos) {
-      p = P.pos[n * P.axes + axis];
-    } else if (P.axes == 1) {
-      p = int(n);
-    } else {
-      const int r = int(n), row = r / P.grid_w;
-      p = axis == 2 ? r - row * P.grid_w : axis == 1 ? row % P.grid_h : row / P.grid_h;
+  const int end = P.n - n0 < P.tokens ? int(P.n - n0) : P.tokens;
+  const int group = threadIdx.x / P.units, u = threadIdx.x - group * P.units;
+  const int tg = group / P.head_groups, hg = group - tg * P.head_groups;
+  const bool rot = u < P.rot_units;
+  // where the unit sits in the head, and its second vector (half layout) P.pairs further on
+  const int c0 = HALF && !rot ? 2 * P.rot_units * EV + (u - P.rot_units) * EV : u * EV;
+  const int step = P.head_groups * P.head_dim;
+  if constexpr (ASYNC) {
+    V* v = mine;
+    for (int tok = tg; tok < end; tok += P.token_groups) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const T* x = static_cast<const T*>(P.src[w]) + (n0 + tok) * P.src_ld[w] + hg * P.head_dim + c0;
+        for (int h = hg; h < P.heads[w]; h += P.head_groups, x += step, v += kVecs * blockDim.x) {
+          copy_async<sizeof(V)>(v, x);
+          if (HALF && rot) copy_async<sizeof(V)>(v + blockDim.x, x + P.pairs);
+        }
+      }
     }
-    const double turns = fma(double(p), P.turn[i], P.start[i]);
-    const float r = float(turns - rint(turns));
-    float s, c;
-    sincospif(2.f * r, &s, &c);
-    cs[x] = make_float2(c * P.m, s * P.m * P.sign);
   }
+  rope_angles(P, n0, end, cosines, sines);
+  if constexpr (ASYNC) asm volatile("cp.async.wait_all;" ::: "memory");  // this thread's own copies
+  __syncthreads();
+  const int valid = MIXED ? min(kPairs, P.pairs - u * kPairs) : kPairs;
+  const V* v = mine;
+  for (int tok = tg; tok < end; tok += P.token_groups) {
+    float co[kPairs], si[kPairs];
+    const int at = tok * P.pairs + u * kPairs;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const bool in = HALF ? rot : !MIXED || i < valid;
+      co[i] = in ? cosines[at + i] : 0.f;
+      si[i] = in ? sines[at + i] : 0.f;
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const T* x = static_cast<const T*>(P.src[w]) + (n0 + tok) * P.src_ld[w] + hg * P.head_dim + c0;
+      T* y = static_cast<T*>(P.dst[w]) + (n0 + tok) * P.dst_ld[w] + hg * P.head_dim + c0;
+#pragma unroll 2
+      for (int h = hg; h < P.heads[w]; h += P.head_groups, x += step, y += step) {
+        V A, B;
+        if constexpr (ASYNC) {
+          A = v[0];
+          if (HALF && rot) B = v[blockDim.x];
+          v += kVecs * blockDim.x;
+        } else if constexpr (ELEM) {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) A.e[e] = x[e];
+        } else {
+          A = *reinterpret_cast<const V*>(x);
+          if (HALF && rot) B = *reinterpret_cast<const V*>(x + P.pairs);
+        }
+        if constexpr (HALF) {
+          if (rot) {
+#pragma unroll
+            for (int e = 0; e < EV; ++e) {
+              const float x1 = to_f(A.e[e]), x2 = to_f(B.e[e]);
+              A.e[e] = from_f<T>(turn1(x1, x2, co[e], si[e]));
+              B.e[e] = from_f<T>(turn2(x1, x2, co[e], si[e]));
+            }
+            *reinterpret_cast<V*>(y + P.pairs) = B;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            const float x1 = to_f(A.e[2 * e]), x2 = to_f(A.e[2 * e + 1]);
+            const T y1 = from_f<T>(turn1(x1, x2, co[e], si[e])), y2 = from_f<T>(turn2(x1, x2, co[e], si[e]));
+            if (!MIXED || e < valid) {  // the others keep their bits, NaN and infinities too
+              A.e[2 * e] = y1;
+              A.e[2 * e + 1] = y2;
+            }
+          }
+        }
+        if constexpr (ELEM) {
+#pragma unroll
+          for (int e = 0; e < EV; ++e) y[e] = A.e[e];
+        } else {
+          *reinterpret_cast<V*>(y) = A;
+        }
+      }
+    }
+  }
+}
+
+// Half layout, rot / 2 any number of elements: 16-byte global accesses of whole
+// rows (addresses, strides and row widths are multiples of 16 bytes), pairs of
+// EV elements rotated in shared memory. `units` threads per head are the
+// rotated ones alone; the other channels pass through with their row.
+template <typename T, int EV>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_staged_kernel(const __grid_constant__ RopeArgs P) {
+  using V = Vec<T, EV>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* const cosines = reinterpret_cast<float*>(smem);
+  float* const sines = cosines + P.tokens * P.pairs;
+  T* const rows = reinterpret_cast<T*>(smem + P.vec_offset);  // [tokens][heads of Q, heads of K][head_dim]
+  const int heads = P.heads[0] + P.heads[1], width = heads * P.head_dim;
+  const int64_t n0 = int64_t(blockIdx.x) * P.tokens;
+  const int end = P.n - n0 < P.tokens ? int(P.n - n0) : P.tokens;
+  constexpr int kE = 16 / sizeof(T);
+  const int vecs[2] = {P.heads[0] * P.head_dim / kE, P.heads[1] * P.head_dim / kE};
+  for (int tok = 0; tok < end; ++tok)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const T* x = static_cast<const T*>(P.src[w]) + (n0 + tok) * P.src_ld[w];
+      T* r = rows + tok * width + (w ? P.heads[0] * P.head_dim : 0);
+      for (int i = threadIdx.x; i < vecs[w]; i += blockDim.x) copy_async<16>(r + i * kE, x + i * kE);
+    }
+  rope_angles(P, n0, end, cosines, sines);
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   const int group = threadIdx.x / P.units, u = threadIdx.x - group * P.units;
   const int tg = group / P.head_groups, hg = group - tg * P.head_groups;
-  constexpr int kPairs = HALF ? EV : EV / 2;  // of a unit
-  const bool rot = u < P.rot_units;
-  // where the unit sits in the head, and its second vector (half layout)
-  const int c0 = HALF && !rot ? 2 * P.rot_units * EV + (u - P.rot_units) * EV : u * EV;
-  const int c1 = HALF && rot ? c0 + P.pairs : c0;
-  // an interleaved vector may hold the last rotated pair and unrotated ones
-  const int valid = rot ? min(kPairs, P.pairs - u * kPairs) : 0;
-  using V = Vec<T, EV>;
-  for (int tok = tg; tok < P.tokens; tok += P.token_groups) {
-    const int64_t n = n0 + tok;
-    if (n >= P.n) break;
-    float co[kPairs], si[kPairs];
+  for (int tok = tg; tok < end; tok += P.token_groups) {
+    float co[EV], si[EV];
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const float2 v = i < valid ? cs[tok * P.pairs + u * kPairs + i] : make_float2(1.f, 0.f);
-      co[i] = v.x;
-      si[i] = v.y;
+    for (int i = 0; i < EV; ++i) {
+      co[i] = cosines[tok * P.pairs + u * EV + i];
+      si[i] = sines[tok * P.pairs + u * EV + i];
     }
-    for (int h0 = hg; h0 < P.heads; h0 += kBatch * P.head_groups) {
-      V a[kBatch], b[kBatch];
+    T* r = rows + tok * width + hg * P.head_dim + u * EV;
+#pragma unroll 2
+    for (int h = hg; h < heads; h += P.head_groups, r += P.head_groups * P.head_dim) {
+      V A = *reinterpret_cast<const V*>(r), B = *reinterpret_cast<const V*>(r + P.pairs);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int h = h0 + j * P.head_groups;
-        if (h < P.heads) {
-          const int w = h >= P.heads_q;
-          const T* s = static_cast<const T*>(P.src[w]) + n * P.src_ld[w] + int64_t(h - (w ? P.heads_q : 0)) * P.head_dim;
-          if constexpr (ELEM) {
-#pragma unroll
-            for (int e = 0; e < EV; ++e) a[j].e[e] = s[c0 + e];
-          } else {
-            a[j] = *reinterpret_cast<const V*>(s + c0);
-            if (HALF && rot) b[j] = *reinterpret_cast<const V*>(s + c1);
-          }
-        }
+      for (int e = 0; e < EV; ++e) {
+        const float x1 = to_f(A.e[e]), x2 = to_f(B.e[e]);
+        A.e[e] = from_f<T>(turn1(x1, x2, co[e], si[e]));
+        B.e[e] = from_f<T>(turn2(x1, x2, co[e], si[e]));
       }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int h = h0 + j * P.head_groups;
-        if (h < P.heads) {
-          const int w = h >= P.heads_q;
-          T* d = static_cast<T*>(P.dst[w]) + n * P.dst_ld[w] + int64_t(h - (w ? P.heads_q : 0)) * P.head_dim;
-          if constexpr (HALF) {
-            if (rot) {
-#pragma unroll
-              for (int e = 0; e < EV; ++e) {
-                const float x = to_f(a[j].e[e]), y = to_f(b[j].e[e]);
-                a[j].e[e] = from_f<T>(x * co[e] - y * si[e]);
-                b[j].e[e] = from_f<T>(y * co[e] + x * si[e]);
-              }
-              *reinterpret_cast<V*>(d + c1) = b[j];
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < kPairs; ++e) {
-              if (e < valid) {  // the others keep their bits, NaN and infinities too
-                const float x = to_f(a[j].e[2 * e]), y = to_f(a[j].e[2 * e + 1]);
-                a[j].e[2 * e] = from_f<T>(x * co[e] - y * si[e]);
-                a[j].e[2 * e + 1] = from_f<T>(y * co[e] + x * si[e]);
-              }
-            }
-          }
-          if constexpr (ELEM) {
-#pragma unroll
-            for (int e = 0; e < EV; ++e) d[c0 + e] = a[j].e[e];
-          } else {
-            *reinterpret_cast<V*>(d + c0) = a[j];
-          }
-        }
-      }
+      *reinterpret_cast<V*>(r) = A;
+      *reinterpret_cast<V*>(r + P.pairs) = B;
     }
   }
+  __syncthreads();
+  for (int tok = 0; tok < end; ++tok)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      T* y = static_cast<T*>(P.dst[w]) + (n0 + tok) * P.dst_ld[w];
+      const T* r = rows + tok * width + (w ? P.heads[0] * P.head_dim : 0);
+      for (int i = threadIdx.x; i < vecs[w]; i += blockDim.x)
+        *reinterpret_cast<uint4*>(y + i * kE) = *reinterpret_cast<const uint4*>(r + i * kE);
+    }
 }
 
 // Turns per position of pair j of an axis with n rotated channels.
@@ -229,28 +346,66 @@ bool rows_meet(uintptr_t a, int64_t sa, int64_t wa, uintptr_t b, int64_t sb, int
   return d < wa || d + wb > sa;
 }
 
-template <typename T, int EV, bool HALF, bool ELEM>
-cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
+// Shared memory of a CTA's vectors.
+int rope_vec_bytes(const RopeArgs& a, int vec, bool half) {
+  const int per_token = (a.heads[0] + a.head_groups - 1) / a.head_groups + (a.heads[1] + a.head_groups - 1) / a.head_groups;
+  const int tokens = (a.tokens + a.token_groups - 1) / a.token_groups;
+  return tokens * per_token * (half ? 2 : 1) * a.units * a.head_groups * a.token_groups * vec;
+}
+
+template <typename T, int EV, bool HALF, bool ELEM, bool MIXED, bool ASYNC>
+cudaError_t launch_as(const RopeArgs& a, int smem, cudaStream_t s) {
   const int64_t ctas = (a.n + a.tokens - 1) / a.tokens;
   const int threads = a.units * a.head_groups * a.token_groups;
-  const size_t smem = size_t(a.tokens) * a.pairs * sizeof(float2);
-  rope_kernel<T, EV, HALF, ELEM><<<unsigned(ctas), threads, smem, s>>>(a);
+  auto kernel = rope_kernel<T, EV, HALF, ELEM, MIXED, ASYNC>;
+  kernel<<<unsigned(ctas), threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
+template <typename T, int EV, bool HALF, bool ELEM, bool MIXED>
+cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
+  const int vec = EV * int(sizeof(T)), bytes = rope_vec_bytes(a, vec, HALF);
+  if constexpr (!ELEM && EV * sizeof(T) >= 4) {
+    if (bytes <= kRopeSmem) return launch_as<T, EV, HALF, ELEM, MIXED, true>(a, a.vec_offset + bytes, s);
+  }
+  return launch_as<T, EV, HALF, ELEM, MIXED, false>(a, a.vec_offset, s);
+}
 template <typename T>
 cudaError_t dispatch(const RopeArgs& a, int ev, bool half, cudaStream_t s) {
   constexpr int kWide = 16 / int(sizeof(T));
   if (!half) {
-    if (ev == kWide) return launch<T, kWide, false, false>(a, s);
-    return launch<T, 2, false, true>(a, s);
+    if (ev != kWide) return launch<T, 2, false, true, true>(a, s);
+    if (a.pairs < a.units * (kWide / 2)) return launch<T, kWide, false, false, true>(a, s);
+    return launch<T, kWide, false, false, false>(a, s);
   }
   if constexpr (kWide == 8) {
-    if (ev == 8) return launch<T, 8, true, false>(a, s);
+    if (ev == 8) return launch<T, 8, true, false, false>(a, s);
   }
-  if (ev == 4) return launch<T, 4, true, false>(a, s);
-  if (ev == 2) return launch<T, 2, true, false>(a, s);
-  return launch<T, 1, true, false>(a, s);
+  if (ev == 4) return launch<T, 4, true, false, false>(a, s);
+  if (ev == 2) return launch<T, 2, true, false, false>(a, s);
+  return launch<T, 1, true, false, false>(a, s);
+}
+
+template <typename T, int EV>
+cudaError_t launch_staged(const RopeArgs& a, int smem, cudaStream_t s) {
+  const int64_t ctas = (a.n + a.tokens - 1) / a.tokens;
+  rope_staged_kernel<T, EV><<<unsigned(ctas), a.units * a.head_groups * a.token_groups, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t dispatch_staged(const RopeArgs& a, int ev, int smem, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (ev == 4) return launch_staged<T, 4>(a, smem, s);
+  }
+  return ev == 2 ? launch_staged<T, 2>(a, smem, s) : launch_staged<T, 1>(a, smem, s);
+}
+
+// x modulo 1 in units of 2^-64 (its two's complement for a negative x).
+uint64_t fraction_bits(double x) {
+  const double r = std::fmod(x, 1.0);
+  const uint64_t b = uint64_t(std::ldexp(std::fabs(r), 64));  // below 2^64: fmod is exact
+  return r < 0.0 ? uint64_t(0) - b : b;
 }
 
 }  // namespace
@@ -314,22 +469,24 @@ extern "C" prism_status prism_rope(const prism_rope_params* params, const prism_
     }
   a.n = n_tokens;
   a.pos = positions;
-  a.heads_q = heads_q;
-  a.heads = heads_q + hk;
+  a.heads[0] = heads_q;
+  a.heads[1] = hk;
   a.head_dim = head_dim;
   a.pairs = rot / 2;
   a.axes = params->n_axes;
   a.pair1 = params->axis_dim[0] / 2;
   a.pair2 = a.axes == 3 ? a.pair1 + params->axis_dim[1] / 2 : a.pairs;
-  a.grid_h = grid ? grid->h : 1;
-  a.grid_w = grid ? grid->w : 1;
+  const bool raster = a.axes == 3 && !positions;
+  a.by_h = fast_div(raster ? grid->h : 1);
+  a.by_w = fast_div(raster ? grid->w : 1);
+  a.by_pairs = fast_div(a.pairs);
   a.m = float(params->magnitude);
   a.sign = transposed ? -1.f : 1.f;
   for (int x = 0, i = 0; x < a.axes; ++x)
     for (int j = 0; j < params->axis_dim[x] / 2; ++j, ++i) {
       const double f = pair_turns(*params, params->axis_dim[x], j);
-      a.turn[i] = params->pos_scale[x] * f;
-      a.start[i] = params->pos_offset[x] * f;
+      a.turn[i] = fraction_bits(params->pos_scale[x] * f);
+      a.start[i] = fraction_bits(params->pos_offset[x] * f);
     }
   // the widest vector that divides the head, the half and every address and stride
   const bool half = params->layout == PRISM_ROPE_HALF;
@@ -343,19 +500,50 @@ extern "C" prism_status prism_rope(const prism_rope_params* params, const prism_
     a.rot_units = (rot + ev - 1) / ev;
     a.units = in_place ? a.rot_units : head_dim / ev;
   }
-  // a CTA: `units` threads per head, as many heads as fit, then tokens side by side
-  a.head_groups = kRopeThreads / a.units < a.heads ? kRopeThreads / a.units : a.heads;
-  a.token_groups = kRopeThreads / (a.units * a.head_groups);
-  // few tokens: a CTA each, for as many SMs as possible
-  int64_t tok = n_tokens / (int64_t(device_sm_count()) * 8);
-  if (tok > kRopeMaxTokens / 2) tok = kRopeMaxTokens / 2;
-  if (tok < 1) tok = 1;
-  if (a.token_groups > kRopeMaxTokens) a.token_groups = kRopeMaxTokens;
-  if (a.token_groups > tok) {
-    if (tok == 1) a.token_groups = 1;
-    else tok = a.token_groups;
+  // a CTA: `units` threads per head, the heads of Q and of K in equal steps, then tokens side by side
+  const int fit = kRopeThreads / a.units < kRopeMaxHeadGroups ? kRopeThreads / a.units : kRopeMaxHeadGroups;
+  a.head_groups = 1;
+  int best = 1 << 30;
+  for (int g = 1; g <= fit; ++g) {  // the fewest idle places, then the fewest steps
+    const int idle = (g - heads_q % g) % g + (hk ? (g - hk % g) % g : 0);
+    if (idle <= best) {
+      best = idle;
+      a.head_groups = g;
+    }
   }
-  a.tokens = int(tok);
+  a.token_groups = kRopeThreads / (a.units * a.head_groups);
+  // tokens of a CTA: its vectors fill kRopeSmem; few tokens: fewer, for as many SMs as possible
+  int64_t tok = n_tokens / (int64_t(device_sm_count()) * 2);
+  if (tok < 1) tok = 1;
+  if (tok > kRopeMaxTokens) tok = kRopeMaxTokens;
+  if (a.token_groups > tok) a.token_groups = int(tok);
+  a.tokens = a.token_groups;
+  const int vec = ev * int(es);
+  while (a.tokens + a.token_groups <= tok) {
+    a.tokens += a.token_groups;
+    if (rope_vec_bytes(a, vec, half) > kRopeSmem) {
+      a.tokens -= a.token_groups;
+      break;
+    }
+  }
+  while (a.token_groups > 1 && rope_vec_bytes(a, vec, half) > kRopeSmem) a.tokens = --a.token_groups;
+  // a half of no whole vectors, rows of whole vectors: through shared memory
+  const int64_t row = int64_t(heads_q + hk) * head_dim * es;
+  const bool staged = half && vec < 16 && bits % 16 == 0 && (int64_t(heads_q) * head_dim * es) % 16 == 0 &&
+                      (int64_t(hk) * head_dim * es) % 16 == 0 && row <= kRopeSmem;
+  if (staged) {
+    a.units = a.rot_units;
+    a.head_groups = std::min(std::min(kRopeThreads / a.units, heads_q + hk), kRopeMaxHeadGroups);
+    a.token_groups = int(std::min<int64_t>(kRopeThreads / (a.units * a.head_groups), tok));
+    a.tokens = int(std::min<int64_t>(tok, kRopeSmem / row));
+    if (a.token_groups > a.tokens) a.token_groups = a.tokens;
+  }
+  a.vec_offset = (a.tokens * a.pairs * 8 + 15) / 16 * 16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (staged) {
+    const int smem = a.vec_offset + a.tokens * int(row);
+    return cuda_status(dtype == PRISM_BF16 ? dispatch_staged<__nv_bfloat16>(a, ev, smem, s)
+                                           : dispatch_staged<float>(a, ev, smem, s));
+  }
   return cuda_status(dtype == PRISM_BF16 ? dispatch<__nv_bfloat16>(a, ev, half, s) : dispatch<float>(a, ev, half, s));
 }

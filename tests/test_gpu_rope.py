@@ -47,6 +47,11 @@ CASES = [
     ((10, 6, 2), 48, 5, 2, (1, 9, 31)),
     ((86, 86, 84), 256, 2, 2, (4, 4, 9)),
     ((6, 10, 10), 80, 32, 8, (2, 17, 33)),
+    # halves of 13, 18 and 20 channels under many tokens; a token of more than a CTA's shared memory
+    ((10, 8, 8), 64, 3, 1, (17, 9, 11)),
+    ((12, 12, 12), 40, 6, 2, (5, 21, 40)),
+    ((20, 10, 10), 64, 20, 4, (16, 20, 16)),
+    ((84, 84, 86), 256, 50, 10, (1, 3, 5)),
 ]
 
 
