@@ -166,8 +166,8 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
   std::memset(&P, 0, sizeof(P));
   P.status = ws_status(ws);
   P.save = dw;
-  P.gate = static_cast<const __nv_bfloat16*>(gate);
-  P.up = static_cast<const __nv_bfloat16*>(up);
+  if ((st = gemm_piece_map(&P.in[0], gate, m, f, f)) != PRISM_OK || (st = gemm_piece_map(&P.in[1], up, m, f, f)) != PRISM_OK)
+    return st;
   GemmProblem g;
   g.a[0] = {dy, dy_stride};
   g.b[0] = {w->w_down, w->down_stride};

@@ -10,19 +10,25 @@
 // dg Wg + du Wu), and a launch may hold several products of the same kind (the
 // three weight gradients).
 //
-// Tiles. CG = 2: a pair of CTAs on neighbouring SMs computes 256 x BN: each
-// holds 128 rows of A and half of B's rows, and the tensor cores of both read
-// both halves of B, so a k-slice of 64 costs each SM 32 KB from L2 for 256 x 256
-// x 64 / 2 multiply-adds (512 tensor cycles): 64 bytes per cycle and SM, where
-// one CTA with a 128 x 256 tile would need 96. CG = 1: one CTA, 128 x BN, for
+// Tiles. What the tensor cores can be fed from L2 decides (measured: about 55
+// bytes per cycle and SM at 1.5 GHz). CG = 2: a pair of CTAs on neighbouring SMs
+// computes 256 rows; each holds 128 rows of A and half of B's rows, and the
+// tensor cores of both read both halves of B. SUB = 2: a tile is two
+// accumulators of 256 columns that share A's slice, 256 x 512 in all: a slice
+// of 64 k costs an SM 48 KB for 1024 tensor cycles, 48 bytes per cycle (64 with
+// 256 x 256, 96 with one CTA's 128 x 256). CG = 1: one CTA, 128 x BN, for
 // products of few tiles.
 //
-// Roles of a CTA's six warps: 0 issues the copies into a ring of kStages
-// slices; 1 owns the tensor memory and issues the products (of the pair: the
-// leader's); 2..5 read the accumulator (a thread per row), apply the epilogue
-// and store 32 x 64 tiles by TMA. Two accumulators: the epilogue of one tile
-// runs beside the products of the next. Persistent CTAs walk the tiles in
-// groups of kGroupM tile rows, whose operands then stay in L2.
+// Roles of a CTA's ten warps: 0 issues the copies into a ring of slices; 1
+// owns the tensor memory and issues the products (of the pair: the leader's);
+// 2..9 read the accumulators (a thread per row, two warps per row alternating
+// over 32-column pieces), apply the epilogue and store 32 x 32 pieces by TMA.
+// SUB = 1: the two accumulators alternate, the epilogue of a tile runs beside
+// the products of the next. SUB = 2: the next tile's first slices are
+// multiplied into the first accumulator while the second is still being read.
+// Persistent CTAs walk the tiles in groups of kGemmGroupM tile rows, whose
+// operands then stay in L2; when the last round has work for less than half of
+// the CTAs, its tiles are split into their two accumulators.
 #pragma once
 #include "host.h"
 #include "ptx.cuh"
@@ -31,13 +37,15 @@ namespace prism {
 
 constexpr int kGemmM = 128;    // rows of A per CTA
 constexpr int kGemmK = 64;     // a slice of K: one 128-byte swizzle row
-constexpr int kGemmStages = 5;
-constexpr int kGemmEpiWarps = 4;
+constexpr int kGemmEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
-constexpr int kGemmOutTile = 32 * 128;  // 32 rows x 64 bf16
-constexpr int kGemmOutTiles = 3;        // per epilogue warp
-constexpr int kGemmGroupM = 8;
+constexpr int kGemmPiece = 32;                      // columns of an epilogue piece
+constexpr int kGemmPieceBytes = 32 * kGemmPiece * 2;  // 32 rows x 32 bf16, 64-byte swizzle
+constexpr int kGemmOutPieces = 2;                   // staging ring of an epilogue warp
+// tile rows per group: 4 to 20 measured on [16384, 4096] x [11264, 4096], 12 best by 1 to 3 %
+constexpr int kGemmGroupM = 12;
 constexpr int kGemmProducts = 3;
+constexpr int kGemmMaxSmem = 232448;
 
 // What happens to the accumulator.
 enum GemmEpilogue : int {
@@ -50,28 +58,36 @@ struct GemmProduct {
   CUtensorMap a[2], b[2];  // by segment of K; kEpiGate: b[0] = Wg, b[1] = Wu
   CUtensorMap out[3];
   int m, n;                // rows and columns of the outputs
-  int tiles_m, tiles_n, tile0;
+  int tiles_m, tiles_n;    // tile columns are of SUB accumulators
+  int subs_n;              // accumulators over the columns
+  int tile0;
   int slices0, slices;     // of segment 0, of both
 };
 
 struct GemmArgs {
   GemmProduct p[kGemmProducts];
-  int products, tiles;
-  int act, save;
-  const __nv_bfloat16 *gate, *up;  // kEpiGateBwd: [m, n], contiguous
+  CUtensorMap in[2];  // kEpiGateBwd: the saved projections, 32 x 32 pieces
+  int products;
+  int whole, units;   // tiles taken whole; these and the halves of the others
+  int save;
   int* status;
 };
 
-template <int CG, int BN>
+template <int CG, int BN, int SUB, int EPI>
 struct GemmLayout {
   static constexpr int kA = kGemmM * 128;
   static constexpr int kB = BN / CG * 128;
-  static constexpr int kStage = kA + kB;
-  static constexpr int kOut = kGemmStages * kStage;
-  static constexpr int kBars = kOut + kGemmEpiWarps * kGemmOutTiles * kGemmOutTile;
-  static constexpr int kSmem = kBars + 256 + 1024;
+  static constexpr int kStage = kA + SUB * kB;
+  static constexpr int kOutBytes = kGemmEpiWarps * kGemmOutPieces * kGemmPieceBytes;
+  static constexpr int kInBytes = EPI == kEpiGateBwd ? kGemmEpiWarps * 2 * kGemmPieceBytes : 0;
+  static constexpr int kFit = (kGemmMaxSmem - 1024 - 512 - kOutBytes - kInBytes) / kStage;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kOut = kStages * kStage;
+  static constexpr int kIn = kOut + kOutBytes;
+  static constexpr int kBars = kIn + kInBytes;
+  static constexpr int kSmem = kBars + 512 + 1024;
   static constexpr int kCols = 2 * BN;  // tensor memory columns
-  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kSmem <= kGemmMaxSmem && kStages >= 3, "shared memory");
   static_assert(kCols <= 512, "tensor memory");
 };
 
@@ -205,13 +221,18 @@ __device__ __forceinline__ void bulk_wait_read() {
 }
 
 // ---------------------------------------------------------------- the kernel
-// Tile t of a launch: its product, tile row and tile column (groups of
-// kGemmGroupM tile rows, tile column by tile column).
-struct GemmTile {
-  int product, tm, tn;
+// Unit u of a launch's work: product, tile row, the first of its accumulators'
+// columns and how many (groups of kGemmGroupM tile rows, tile column by tile
+// column). Units from P.whole on are halves of tiles (an empty one where a tile
+// has one accumulator only).
+struct GemmUnit {
+  int product, tm, sub, subs;
 };
-__device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& P, int t) {
-  GemmTile r;
+template <int SUB>
+__device__ __forceinline__ GemmUnit gemm_unit(const GemmArgs& P, int u) {
+  const bool half = SUB == 2 && u >= P.whole;
+  int t = half ? P.whole + ((u - P.whole) >> 1) : u;
+  GemmUnit r;
   r.product = 0;
   while (r.product + 1 < P.products && t >= P.p[r.product + 1].tile0) ++r.product;
   const GemmProduct& Q = P.p[r.product];
@@ -219,8 +240,10 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmArgs& P, int t) {
   const int per = kGemmGroupM * Q.tiles_n, g = t / per;
   const int rows = min(kGemmGroupM, Q.tiles_m - g * kGemmGroupM);
   t -= g * per;
-  r.tn = t / rows;
-  r.tm = g * kGemmGroupM + (t - r.tn * rows);
+  const int tn = t / rows;
+  r.tm = g * kGemmGroupM + (t - tn * rows);
+  r.sub = tn * SUB + (half ? (u - P.whole) & 1 : 0);
+  r.subs = max(0, min(half ? 1 : SUB, Q.subs_n - r.sub));
   return r;
 }
 
@@ -234,105 +257,123 @@ __device__ __forceinline__ void gemm_load(uint32_t dst, const CUtensorMap* map, 
   }
 }
 
-// 32 bf16 values (packed) to half `half` of row `lane` of a 32 x 64 tile.
-__device__ __forceinline__ void stage32(uint8_t* tile, int lane, int half, const uint32_t* w) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(tile + sw128_offset(lane, half * 4 + c)) =
-        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+// Byte offset of 16-byte chunk `chunk` of row `row` of a 32 x 32 piece (rows of
+// 64 bytes, 64-byte swizzle).
+__device__ __forceinline__ uint32_t piece_offset(uint32_t row, uint32_t chunk) {
+  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
 }
 
-// The epilogue of one 32-row, 64-column piece: columns `col` of the outputs,
-// accumulator columns at `acc` (kEpiGate: u's at acc + BN / 2).
-template <int BN, int EPI, int ACT>
-__device__ __forceinline__ void gemm_piece(const GemmArgs& P, const GemmProduct& Q, uint32_t acc, uint8_t* tiles,
-                                           int lane, int row, int col) {
-  const bool row_in = row + lane < Q.m;
+// An epilogue warp's staging ring: pieces leave by TMA stores, each waited for
+// (until read) before its place is written again.
+struct PieceRing {
+  uint8_t* base;
+  int at;
+  __device__ __forceinline__ void store(const CUtensorMap* map, const uint32_t* w, int lane, int row, int col) {
+    uint8_t* p = base + at * kGemmPieceBytes;
+    at = at + 1 == kGemmOutPieces ? 0 : at + 1;
+    if (lane == 0) bulk_wait_read<kGemmOutPieces - 1>();
+    __syncwarp();
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t r[32], w[16];
-    if constexpr (EPI == kEpiStore) {
-      tmem_ld32(acc + half * 32, r);
-      tmem_ld_wait();
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint4*>(p + piece_offset(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, smem_u32(p), col, row);
+      bulk_commit_group();
+    }
+  }
+};
+
+__device__ __forceinline__ void pack32(const uint32_t* r, uint32_t* w) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-      stage32(tiles, lane, half, w);
-    } else if constexpr (EPI == kEpiGate) {
-      uint32_t u[32];
-      tmem_ld32(acc + half * 32, r);
-      tmem_ld32(acc + BN / 2 + half * 32, u);
-      tmem_ld_wait();
-      if (P.save) {
+  for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+
+// kEpiStore, kEpiGate: the outputs of one 32-row, 32-column piece from its
+// accumulator values r (kEpiGate: of g, and u of u).
+template <int EPI, int ACT>
+__device__ __forceinline__ void gemm_piece(const GemmArgs& P, const GemmProduct& Q, const uint32_t* r, const uint32_t* u,
+                                           PieceRing& ring, int lane, int row, int col) {
+  uint32_t w[16];
+  if constexpr (EPI == kEpiStore) {
+    pack32(r, w);
+    ring.store(&Q.out[0], w, lane, row, col);
+  } else {
+    // h from the fp32 projections, rounded once
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        stage32(tiles + kGemmOutTile, lane, half, w);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-        stage32(tiles + 2 * kGemmOutTile, lane, half, w);
-      }
-      // h from the fp32 projections, rounded once
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        w[i] = pack_bf16x2(act_f<ACT>(__uint_as_float(r[2 * i])) * __uint_as_float(u[2 * i]),
-                           act_f<ACT>(__uint_as_float(r[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
-      stage32(tiles, lane, half, w);
-    } else {
-      // the saved projections of this row's 32 columns
-      uint4 gv[4], uv[4];
-      const size_t at = size_t(row + lane) * Q.n + col + half * 32;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool in = row_in && col + half * 32 + 8 * c < Q.n;
-        gv[c] = in ? __ldg(reinterpret_cast<const uint4*>(P.gate + at) + c) : make_uint4(0, 0, 0, 0);
-        uv[c] = in ? __ldg(reinterpret_cast<const uint4*>(P.up + at) + c) : make_uint4(0, 0, 0, 0);
-      }
-      tmem_ld32(acc + half * 32, r);
-      tmem_ld_wait();
-      uint32_t wg[16], wu[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t g2 = reinterpret_cast<const uint32_t*>(gv)[i], u2 = reinterpret_cast<const uint32_t*>(uv)[i];
-        float dg[2], du[2], h[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float g = __uint_as_float(e ? g2 & 0xFFFF0000u : g2 << 16);
-          const float u = __uint_as_float(e ? u2 & 0xFFFF0000u : u2 << 16);
-          const float dh = __uint_as_float(r[2 * i + e]);
-          float a, s;
-          act_slope_f<ACT>(g, a, s);
-          dg[e] = dh * u * s;
-          du[e] = dh * a;
-          h[e] = a * u;
-        }
-        wg[i] = pack_bf16x2(dg[0], dg[1]);
-        wu[i] = pack_bf16x2(du[0], du[1]);
-        w[i] = pack_bf16x2(h[0], h[1]);
-      }
-      stage32(tiles, lane, half, wg);
-      stage32(tiles + kGemmOutTile, lane, half, wu);
-      if (P.save) stage32(tiles + 2 * kGemmOutTile, lane, half, w);
+    for (int i = 0; i < 16; ++i)
+      w[i] = pack_bf16x2(act_f<ACT>(__uint_as_float(r[2 * i])) * __uint_as_float(u[2 * i]),
+                         act_f<ACT>(__uint_as_float(r[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+    ring.store(&Q.out[0], w, lane, row, col);
+    if (P.save) {
+      pack32(r, w);
+      ring.store(&Q.out[1], w, lane, row, col);
+      pack32(u, w);
+      ring.store(&Q.out[2], w, lane, row, col);
     }
   }
 }
 
-template <int CG, int BN, bool AMN, bool BMN, int EPI, int ACT>
+// kEpiGateBwd: the outputs of one piece from dh in tensor memory at `acc` and
+// the saved projections' piece at `in` (gate, then up); `taken` once that is read.
+template <int ACT, typename F>
+__device__ __forceinline__ void gemm_piece_bwd(const GemmArgs& P, const GemmProduct& Q, uint32_t acc, PieceRing& ring,
+                                               const uint8_t* in, int lane, int row, int col, const F& taken) {
+  uint32_t r[32], w[16], wg[16], wu[16];
+  tmem_ld32(acc, r);
+  uint4 gv[4], uv[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    gv[c] = *reinterpret_cast<const uint4*>(in + piece_offset(lane, c));
+    uv[c] = *reinterpret_cast<const uint4*>(in + kGemmPieceBytes + piece_offset(lane, c));
+  }
+  __syncwarp();
+  taken();
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t g2 = reinterpret_cast<const uint32_t*>(gv)[i], u2 = reinterpret_cast<const uint32_t*>(uv)[i];
+    float dg[2], du[2], h[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float g = __uint_as_float(e ? g2 & 0xFFFF0000u : g2 << 16);
+      const float u = __uint_as_float(e ? u2 & 0xFFFF0000u : u2 << 16);
+      const float dh = __uint_as_float(r[2 * i + e]);
+      float a, s;
+      act_slope_f<ACT>(g, a, s);
+      dg[e] = dh * u * s;
+      du[e] = dh * a;
+      h[e] = a * u;
+    }
+    wg[i] = pack_bf16x2(dg[0], dg[1]);
+    wu[i] = pack_bf16x2(du[0], du[1]);
+    w[i] = pack_bf16x2(h[0], h[1]);
+  }
+  ring.store(&Q.out[0], wg, lane, row, col);
+  ring.store(&Q.out[1], wu, lane, row, col);
+  if (P.save) ring.store(&Q.out[2], w, lane, row, col);
+}
+
+template <int CG, int BN, int SUB, bool AMN, bool BMN, int EPI, int ACT>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs P) {
-  using L = GemmLayout<CG, BN>;
+  using L = GemmLayout<CG, BN, SUB, EPI>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBars);  // slice landed (leader's: of both CTAs)
-  uint64_t* empty = full + kGemmStages;                         // slice's products complete
-  uint64_t* acc_full = empty + kGemmStages;                     // [2] a tile's products complete
+  uint64_t* empty = full + L::kStages;                          // slice's products complete
+  uint64_t* acc_full = empty + L::kStages;                      // [2] an accumulator's products complete
   uint64_t* acc_empty = acc_full + 2;                           // [2] accumulator read (leader's: by both CTAs)
   uint64_t* mma_done = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(mma_done + 2);
+  uint64_t* in_full = mma_done + 1;                             // [epilogue warps] saved projections landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + kGemmEpiWarps);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
   int* status = P.status;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kGemmStages; ++i) {
+    for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
@@ -341,6 +382,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       mbar_init(&acc_empty[i], CG * kGemmEpiWarps);
     }
     mbar_init(mma_done, 1);
+    for (int i = 0; i < kGemmEpiWarps; ++i) mbar_init(&in_full[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -356,124 +398,182 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     if (lane == 0) {
       bool ok = true;
       int it = 0;
-      for (int t = cluster; t < P.tiles && ok; t += clusters) {
-        const GemmTile T = gemm_tile(P, t);
-        const GemmProduct& Q = P.p[T.product];
-        const int row0 = (T.tm * CG + rank) * kGemmM;
+      for (int u = cluster; u < P.units && ok; u += clusters) {
+        const GemmUnit U = gemm_unit<SUB>(P, u);
+        if (U.subs == 0) continue;
+        const GemmProduct& Q = P.p[U.product];
+        const int row0 = (U.tm * CG + rank) * kGemmM;
         for (int kc = 0; kc < Q.slices; ++kc, ++it) {
-          const int st = it % kGemmStages;
-          if (it >= kGemmStages) ok = mbar_wait_abortable(&empty[st], ((it / kGemmStages) - 1) & 1, status, abort_flag);
+          const int st = it % L::kStages;
+          if (it >= L::kStages) ok = mbar_wait_abortable(&empty[st], ((it / L::kStages) - 1) & 1, status, abort_flag);
           if (!ok) break;
           const int seg = kc >= Q.slices0;
           const int k0 = (kc - (seg ? Q.slices0 : 0)) * kGemmK;
-          const uint32_t dst = smem_u32(sm + st * L::kStage);
+          uint32_t dst = smem_u32(sm + st * L::kStage);
           uint32_t bar = smem_u32(&full[st]);
           if constexpr (CG == 2) bar = map_shared(bar, 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], CG * L::kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], CG * (L::kA + U.subs * L::kB));
           gemm_load<CG, AMN>(dst, &Q.a[seg], bar, row0, k0, kGemmM);
-          if constexpr (EPI == kEpiGate) {
-            const int f0 = T.tn * (BN / 2);
-            if constexpr (CG == 2) {
-              gemm_load<CG, BMN>(dst + L::kA, &Q.b[rank], bar, f0, k0, BN / 2);
+          dst += L::kA;
+          for (int i = 0; i < U.subs; ++i, dst += L::kB) {
+            if constexpr (EPI == kEpiGate) {
+              const int f0 = (U.sub + i) * (BN / 2);
+              if constexpr (CG == 2) {
+                gemm_load<CG, BMN>(dst, &Q.b[rank], bar, f0, k0, BN / 2);
+              } else {
+                gemm_load<CG, BMN>(dst, &Q.b[0], bar, f0, k0, BN / 2);
+                gemm_load<CG, BMN>(dst + BN / 2 * 128, &Q.b[1], bar, f0, k0, BN / 2);
+              }
             } else {
-              gemm_load<CG, BMN>(dst + L::kA, &Q.b[0], bar, f0, k0, BN / 2);
-              gemm_load<CG, BMN>(dst + L::kA + BN / 2 * 128, &Q.b[1], bar, f0, k0, BN / 2);
+              gemm_load<CG, BMN>(dst, &Q.b[seg], bar, (U.sub + i) * BN + int(rank) * (BN / CG), k0, BN / CG);
             }
-          } else {
-            gemm_load<CG, BMN>(dst + L::kA, &Q.b[seg], bar, T.tn * BN + int(rank) * (BN / CG), k0, BN / CG);
           }
         }
       }
       // every copy has landed before a CTA may exit: the leader's barriers count both CTAs' copies
       if (rank == 0)
-        for (int i = it > kGemmStages ? it - kGemmStages : 0; i < it; ++i)
-          mbar_wait(&full[i % kGemmStages], (i / kGemmStages) & 1, status);
+        for (int i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
+          mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1, status);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = idesc_bf16_f32(kGemmM * CG, BN, AMN, BMN);
       constexpr uint64_t kStepA = (AMN ? 2048 : 32) >> 4, kStepB = (BMN ? 2048 : 32) >> 4;  // 16 values of K
+      // slice in ring place st, times B's rows of accumulator `sub`; K-major: 8-row groups 1024 bytes apart;
+      // MN-major: 64-value boxes 8192 bytes apart, 8-k groups 1024
+      auto multiply = [&](int st, int sub, uint32_t d, bool first) {
+        const uint32_t sa = smem_u32(sm + st * L::kStage);
+        const uint64_t da = sdesc_sw128(sa, AMN ? 8192 : 16, 1024);
+        const uint64_t db = sdesc_sw128(sa + L::kA + sub * L::kB, BMN ? 8192 : 16, 1024);
+#pragma unroll
+        for (int k = 0; k < kGemmK / 16; ++k)
+          mma_bf16<CG>(d, da + k * kStepA, db + k * kStepB, idesc, (!first || k > 0) ? 1u : 0u);
+      };
       bool ok = true;
-      int it = 0, lt = 0;
-      for (int t = cluster; t < P.tiles && ok; t += clusters, ++lt) {
-        const int acc = lt & 1;
-        if (lt >= 2) ok = mbar_wait_abortable(&acc_empty[acc], ((lt >> 1) - 1) & 1, status, abort_flag);
+      int it = 0, j = 0;  // slices, accumulators so far
+      for (int u = cluster; u < P.units && ok; u += clusters) {
+        const GemmUnit U = gemm_unit<SUB>(P, u);
+        if (U.subs == 0) continue;
+        const int slices = P.p[U.product].slices;
+        const int acc = j & 1;
+        const uint32_t d0 = tbase + acc * BN, d1 = tbase + (acc ^ 1) * BN;
+        if (j >= 2) ok = mbar_wait_abortable(&acc_empty[acc], ((j >> 1) - 1) & 1, status, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tbase + acc * BN;
-        const int slices = P.p[gemm_tile(P, t).product].slices;
-        for (int kc = 0; kc < slices; ++kc, ++it) {
-          const int st = it % kGemmStages;
-          ok = mbar_wait_abortable(&full[st], (it / kGemmStages) & 1, status, abort_flag);
+        int kc = 0;
+        if (SUB == 2 && U.subs == 2) {
+          // the first slices into the first accumulator, while the second may still be read
+          const int pre = min(slices, L::kStages);
+          for (; kc < pre; ++kc) {
+            ok = mbar_wait_abortable(&full[(it + kc) % L::kStages], ((it + kc) / L::kStages) & 1, status, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            multiply((it + kc) % L::kStages, 0, d0, kc == 0);
+            if (kc == slices - 1) mma_commit_all<CG>(&acc_full[acc]);
+          }
+          if (!ok) break;
+          if (j + 1 >= 2) ok = mbar_wait_abortable(&acc_empty[acc ^ 1], (((j + 1) >> 1) - 1) & 1, status, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(sm + st * L::kStage);
-          // K-major: 8-row groups 1024 bytes apart; MN-major: 64-value boxes 8192 bytes apart, 8-k groups 1024
-          const uint64_t da = sdesc_sw128(sa, AMN ? 8192 : 16, 1024), db = sdesc_sw128(sa + L::kA, BMN ? 8192 : 16, 1024);
-#pragma unroll
-          for (int k = 0; k < kGemmK / 16; ++k)
-            mma_bf16<CG>(d, da + k * kStepA, db + k * kStepB, idesc, (kc > 0 || k > 0) ? 1u : 0u);
+          for (kc = 0; kc < pre; ++kc, ++it) {
+            multiply(it % L::kStages, 1, d1, kc == 0);
+            mma_commit_all<CG>(&empty[it % L::kStages]);
+          }
+        }
+        for (; kc < slices; ++kc, ++it) {
+          const int st = it % L::kStages;
+          ok = mbar_wait_abortable(&full[st], (it / L::kStages) & 1, status, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          multiply(st, 0, d0, kc == 0);
+          if (kc == slices - 1) mma_commit_all<CG>(&acc_full[acc]);
+          if (SUB == 2 && U.subs == 2) multiply(st, 1, d1, false);
           mma_commit_all<CG>(&empty[st]);
         }
-        if (ok) mma_commit_all<CG>(&acc_full[acc]);
+        if (ok && U.subs == 2) mma_commit_all<CG>(&acc_full[acc ^ 1]);
+        j += U.subs;
       }
       // every product has completed before the tensor memory is released
-      if constexpr (CG == 2) mma_commit_all<CG>(mma_done);
-      else mma_commit(mma_done);
+      mma_commit_all<CG>(mma_done);
       mbar_wait(mma_done, 0, status);
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;  // tensor memory lane quarter
-    uint8_t* tiles = sm + L::kOut + (warp - 2) * kGemmOutTiles * kGemmOutTile;
-    constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;  // output columns of a tile
-    int lt = 0, ring = 0;
-    for (int t = cluster; t < P.tiles; t += clusters, ++lt) {
-      const GemmTile T = gemm_tile(P, t);
-      const GemmProduct& Q = P.p[T.product];
-      const int row = (T.tm * CG + int(rank)) * kGemmM + 32 * q, col0 = T.tn * kCols;
-      const int acc = lt & 1;
-      if (!mbar_wait_abortable(&acc_full[acc], (lt >> 1) & 1, status, abort_flag)) break;
-      tc_fence_after();
-      if (row < Q.m) {
-#pragma unroll 1
-        for (int c = 0; c < kCols && col0 + c < Q.n; c += 64) {
-          // the tiles' last stores have been read: one tile a piece in a ring of three, or all three
-          uint8_t* dst = tiles;
-          if constexpr (EPI == kEpiStore) {
-            dst = tiles + ring * kGemmOutTile;
-            ring = ring == kGemmOutTiles - 1 ? 0 : ring + 1;
-            if (lane == 0) bulk_wait_read<kGemmOutTiles - 1>();
-          } else {
-            if (lane == 0) bulk_wait_read<0>();
-          }
-          __syncwarp();
-          gemm_piece<BN, EPI, ACT>(P, Q, tbase + acc * BN + (uint32_t(q * 32) << 16) + c, dst, lane, row, col0 + c);
-          fence_proxy_async_smem();
+    const int q = warp & 3;           // tensor memory lane quarter
+    const int e = warp - 2;
+    const int c0 = (e >> 2) * kGemmPiece;  // of the two warps of a quarter, one takes the even pieces, one the odd
+    PieceRing ring = {sm + L::kOut + e * kGemmOutPieces * kGemmPieceBytes, 0};
+    uint8_t* in = sm + L::kIn + e * 2 * kGemmPieceBytes;  // gate, up
+    uint64_t* in_bar = in_full + e;
+    constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;  // output columns of an accumulator
+    constexpr int kMine = kCols / (2 * kGemmPiece);       // pieces of this warp
+    int j = 0, pieces = 0;
+    bool ok = true;
+    for (int u = cluster; u < P.units && ok; u += clusters) {
+      const GemmUnit U = gemm_unit<SUB>(P, u);
+      const GemmProduct& Q = P.p[U.product];
+      const int row = (U.tm * CG + int(rank)) * kGemmM + 32 * q;
+      for (int i = 0; i < U.subs; ++i, ++j) {
+        const int col = (U.sub + i) * kCols, acc = j & 1;
+        const int end = row < Q.m ? min(kCols, Q.n - col) : 0;
+        const uint32_t t_acc = tbase + acc * BN + (uint32_t(q * 32) << 16) + c0;
+        auto wait_acc = [&]() {
+          ok = __all_sync(0xffffffffu, mbar_wait_abortable(&acc_full[acc], (j >> 1) & 1, status, abort_flag));
+          tc_fence_after();
+          return ok;
+        };
+        auto release_acc = [&]() {
+          tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            const uint32_t src = smem_u32(dst);
-            tma_store_2d(&Q.out[0], src, col0 + c, row);
-            if (EPI == kEpiGateBwd || (EPI == kEpiGate && P.save))
-              tma_store_2d(&Q.out[1], src + kGemmOutTile, col0 + c, row);
-            if (EPI != kEpiStore && P.save) tma_store_2d(&Q.out[2], src + 2 * kGemmOutTile, col0 + c, row);
-            bulk_commit_group();
+            if constexpr (CG == 2) mbar_arrive_cluster(map_shared(smem_u32(&acc_empty[acc]), 0));
+            else mbar_arrive(&acc_empty[acc]);
+          }
+        };
+        if constexpr (EPI == kEpiGateBwd) {
+          auto fetch = [&](int c) {  // the saved projections of the piece at column c
+            if (c < end && lane == 0) {
+              mbar_arrive_expect_tx(in_bar, 2 * kGemmPieceBytes);
+              tma_load_2d<1>(smem_u32(in), &P.in[0], smem_u32(in_bar), col + c, row);
+              tma_load_2d<1>(smem_u32(in) + kGemmPieceBytes, &P.in[1], smem_u32(in_bar), col + c, row);
+            }
+          };
+          fetch(c0);
+          if (!wait_acc()) break;
+#pragma unroll 1
+          for (int c = c0; c < end; c += 2 * kGemmPiece, ++pieces) {
+            ok = __all_sync(0xffffffffu, mbar_wait_abortable(in_bar, pieces & 1, status, abort_flag));
+            if (!ok) break;
+            gemm_piece_bwd<ACT>(P, Q, t_acc + (c - c0), ring, in, lane, row, col + c,
+                                [&]() { fetch(c + 2 * kGemmPiece); });
+          }
+          if (!ok) break;
+          release_acc();
+        } else {
+          // all of this warp's values into registers, so that the accumulator is free at once
+          if (!wait_acc()) break;
+          uint32_t r[kMine][32], v[EPI == kEpiGate ? kMine : 1][32];
+#pragma unroll
+          for (int p = 0; p < kMine; ++p) {
+            tmem_ld32(t_acc + p * 2 * kGemmPiece, r[p]);
+            if constexpr (EPI == kEpiGate) tmem_ld32(t_acc + BN / 2 + p * 2 * kGemmPiece, v[p]);
+          }
+          tmem_ld_wait();
+          release_acc();
+#pragma unroll
+          for (int p = 0; p < kMine; ++p) {
+            const int c = c0 + p * 2 * kGemmPiece;
+            if (c < end) gemm_piece<EPI, ACT>(P, Q, r[p], v[EPI == kEpiGate ? p : 0], ring, lane, row, col + c);
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2) mbar_arrive_cluster(map_shared(smem_u32(&acc_empty[acc]), 0));
-        else mbar_arrive(&acc_empty[acc]);
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
-  if constexpr (CG == 2) {
-    // a pair that gave up may leave copies of the other CTA on their way: let them land
+  if (CG == 2 || EPI == kEpiGateBwd) {
+    // a CTA that gave up may leave copies of its own or of its pair on their way: let them land
     if (*abort_flag) {
       const uint64_t t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 1000000) {
