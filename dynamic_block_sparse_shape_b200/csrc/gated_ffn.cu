@@ -96,6 +96,7 @@ extern "C" prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t 
   if (m == 0) return PRISM_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void* h = static_cast<uint8_t*>(ws) + kWsHeader;
+  if (m <= kRowTokens) return ffn_rows_forward(act, *w, int(m), x, x_stride, h, y, y_stride, gate, up, s);
   GemmArgs P;
   std::memset(&P, 0, sizeof(P));
   P.status = ws_status(ws);
@@ -114,6 +115,7 @@ extern "C" prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t 
   r.b[0] = {w->w_down, w->down_stride};
   r.out[0] = {y, y_stride};
   r.m = m; r.n = d; r.k[0] = f;
+  P.follows = 1;
   return ffn_product_nt(P, r, s);
 }
 
@@ -166,16 +168,17 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
   std::memset(&P, 0, sizeof(P));
   P.status = ws_status(ws);
   P.save = dw;
-  if ((st = gemm_piece_map(&P.in[0], gate, m, f, f)) != PRISM_OK || (st = gemm_piece_map(&P.in[1], up, m, f, f)) != PRISM_OK)
-    return st;
   GemmProblem g;
   g.a[0] = {dy, dy_stride};
+  g.in[0] = gate;
+  g.in[1] = up;
   g.b[0] = {w->w_down, w->down_stride};
   g.out[0] = {dg, f};
   g.out[1] = {du, f};
   g.out[2] = {h, f};
   g.m = m; g.n = f; g.k[0] = d;
   if ((st = ffn_gate_bwd_product(act, P, g, s)) != PRISM_OK) return st;
+  P.follows = 1;
   if (dx) {
     GemmProblem r;
     r.a[0] = {dg, f};

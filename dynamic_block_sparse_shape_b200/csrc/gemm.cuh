@@ -70,6 +70,7 @@ struct GemmArgs {
   int products;
   int whole, units;   // tiles taken whole; these and the halves of the others
   int save;
+  int follows;        // launched behind another product of the same call
   int* status;
 };
 
@@ -93,8 +94,14 @@ struct GemmLayout {
 
 // ---------------------------------------------------------------- activations
 // With e = exp(-z), sigmoid(z) = 1 / (1 + e) keeps its relative precision on
-// either side of 0 (an infinite e gives 0).
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// either side of 0 (an infinite e gives 0). The hardware's exponential and
+// reciprocal (2 ulp and 1 ulp) do: the result is rounded to bf16.
+__device__ __forceinline__ float sigmoid_f(float z) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_f(float g) {
@@ -215,6 +222,12 @@ __device__ __forceinline__ void tmem_dealloc_cg(uint32_t addr, uint32_t cols) {
   else
     tmem_dealloc(addr, cols);
 }
+// Programmatic dependent launch: waits for the kernels that this launch depends
+// on (nothing when it was launched in plain stream order), and lets the next
+// launch set itself up.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
@@ -372,6 +385,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
   int* status = P.status;
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&P.p[0].a[0]);
+    tma_prefetch_desc(&P.p[0].b[0]);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -392,6 +409,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   else __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies

@@ -1,8 +1,10 @@
 // Host side of gemm.cuh: tensor maps, the choice of tiles, the launch.
 #pragma once
+#include <algorithm>
+#include <cmath>
 #include <cstring>
 
-#include "gemm.cuh"
+#include "gemm_split.cuh"
 
 namespace prism {
 
@@ -18,6 +20,7 @@ struct GemmOutput {
 struct GemmProblem {
   GemmOperand a[2], b[2];
   GemmOutput out[3];
+  const void* in[2] = {nullptr, nullptr};  // kEpiGateBwd: the saved projections, contiguous
   int64_t m = 0, n = 0;
   int64_t k[2] = {0, 0};
 };
@@ -36,6 +39,19 @@ inline prism_status gemm_piece_map(CUtensorMap* map, const void* base, int64_t m
   const uint64_t strides[1] = {uint64_t(ld) * 2};
   const uint32_t box[2] = {kGemmPiece, 32};
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// The launch's attributes: the cluster, and for a product that follows another
+// of the same call (P.follows) a programmatic dependence on it, so that its
+// launch and setup run beside the other's end.
+inline void gemm_follow(const GemmArgs& P, cudaLaunchAttribute* at, int n, cudaLaunchConfig_t* cfg) {
+  if (P.follows) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg->attrs = at;
+  cfg->numAttrs = n;
 }
 
 template <int CG, int BN, int SUB, bool AMN, bool BMN, int EPI, int ACT>
@@ -68,6 +84,11 @@ prism_status gemm_launch(GemmArgs& P, const GemmProblem* pr, int products, cudaS
       if (R.out[g].base) st = gemm_piece_map(&Q.out[g], R.out[g].base, R.m, R.n, R.out[g].ld);
     if (st != PRISM_OK) return st;
   }
+  if constexpr (EPI == kEpiGateBwd) {
+    prism_status st = PRISM_OK;
+    for (int g = 0; g < 2 && st == PRISM_OK; ++g) st = gemm_piece_map(&P.in[g], pr[0].in[g], pr[0].m, pr[0].n, pr[0].n);
+    if (st != PRISM_OK) return st;
+  }
   int clusters = device_sm_count() / CG;
   P.whole = tiles;
   if (SUB == 2 && tiles % clusters * 2 <= clusters) P.whole = tiles / clusters * clusters;
@@ -82,34 +103,127 @@ prism_status gemm_launch(GemmArgs& P, const GemmProblem* pr, int products, cudaS
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = CG;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
+  gemm_follow(P, at, 1, &cfg);
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, P));
 }
 
-// Pairs of CTAs when there is an accumulator of 256 x 256 for each of the SMs'
-// pairs; otherwise smaller tiles of single CTAs, as many as possible.
+template <int BN, bool AMN, bool BMN, int EPI, int ACT>
+prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int products, int ranks, cudaStream_t s) {
+  constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;
+  SplitLaunch A;
+  std::memset(&A, 0, sizeof(A));
+  A.products = products;
+  A.save = P.save;
+  A.status = P.status;
+  const int a_rows = AMN || pr[0].m >= kGemmM ? kGemmM : int(pr[0].m + 7) / 8 * 8;
+  A.a_bytes = a_rows * 128;
+  int64_t tiles = 0, slices = 0;
+  for (int i = 0; i < products; ++i) {
+    SplitArgs& Q = A.p[i];
+    const GemmProblem& R = pr[i];
+    Q.m = int(R.m);
+    Q.n = int(R.n);
+    Q.tiles_m = int((R.m + kGemmM - 1) / kGemmM);
+    Q.tiles_n = int((R.n + kCols - 1) / kCols);
+    Q.tile0 = int(tiles);
+    tiles += int64_t(Q.tiles_m) * Q.tiles_n;
+    Q.slices0 = int((R.k[0] + kGemmK - 1) / kGemmK);
+    Q.slices = Q.slices0 + int((R.k[1] + kGemmK - 1) / kGemmK);
+    if (Q.slices > slices) slices = Q.slices;
+    prism_status st = PRISM_OK;
+    for (int g = 0; g < 2 && st == PRISM_OK; ++g) {
+      if (R.a[g].base) st = gemm_operand_map(&Q.a[g], R.a[g], AMN, R.m, R.k[g], a_rows);
+      const int64_t kb = EPI == kEpiGate ? R.k[0] : R.k[g];
+      if (R.b[g].base && st == PRISM_OK) st = gemm_operand_map(&Q.b[g], R.b[g], BMN, R.n, kb, kCols);
+      Q.in[g] = static_cast<const __nv_bfloat16*>(R.in[g]);
+    }
+    if (st != PRISM_OK) return st;
+    for (int g = 0; g < 3; ++g) {
+      Q.out[g] = static_cast<__nv_bfloat16*>(R.out[g].base);
+      Q.out_ld[g] = R.out[g].ld;
+    }
+  }
+  if (tiles * ranks >= (int64_t(1) << 31)) return PRISM_ERR_UNSUPPORTED;
+  // a ring of all of an SM's shared memory, or two of half of it
+  const int room = tiles * ranks <= device_sm_count() ? kGemmMaxSmem : 113 * 1024;
+  A.stages = int(std::min<int64_t>(kSplitStages, (slices + ranks - 1) / ranks));
+  while (A.stages > 1 && split_smem(BN, A.a_bytes, A.stages) > room) --A.stages;
+  const int smem = split_smem(BN, A.a_bytes, A.stages);
+  auto kernel = gemm_split_kernel<BN, AMN, BMN, EPI, ACT>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmMaxSmem) != cudaSuccess)
+    return PRISM_ERR_CUDA;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(unsigned(tiles * ranks));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ranks;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  gemm_follow(P, at, 1, &cfg);
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, A));
+}
+
+// Time of a product in ns by what it is made of: an SM's copy engine takes
+// kRowNs per 128-byte row, a slice's products their tensor cycles, and a round
+// of tiles its fill and epilogue.
+constexpr double kRowNs = 1.8, kLatencyNs = 1500.0, kCycleNs = 1.0 / 1.8, kPairNs = 4000.0, kSplitNs = 3000.0, kSumNs = 1000.0;
+
+// The kernel and tiles for a product: pairs of CTAs for many tiles (SUB = 2
+// shares A's rows; the gradient of the gate has the longest epilogue and
+// alternates its accumulators to hide it), K split over a cluster for few. The
+// times decide, from measured rates; what they are off by shows only where two
+// choices are close.
 template <bool AMN, bool BMN, int EPI, int ACT>
 prism_status gemm(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s) {
   const int sms = device_sm_count();
-  auto tiles = [&](int rows, int cols) {
-    int64_t t = 0;
-    for (int i = 0; i < products; ++i) t += ((pr[i].m + rows - 1) / rows) * ((pr[i].n + cols - 1) / cols);
+  constexpr int kHalf = EPI == kEpiGate ? 2 : 1;
+  constexpr int kSub = EPI == kEpiGateBwd ? 1 : 2;
+  auto tiles = [&](int64_t rows, int64_t cols) {
+    double t = 0;
+    for (int i = 0; i < products; ++i) t += double((pr[i].m + rows - 1) / rows) * double((pr[i].n * kHalf + cols - 1) / cols);
     return t;
   };
-  constexpr int kHalf = EPI == kEpiGate ? 2 : 1;
-  // the gradient of the gate has the longest epilogue: it needs the second accumulator to hide it
-  constexpr int kSub = EPI == kEpiGateBwd ? 1 : 2;
-  if (tiles(256, 256 / kHalf) * 2 >= sms) return gemm_launch<2, 256, kSub, AMN, BMN, EPI, ACT>(P, pr, products, s);
-  if constexpr (EPI != kEpiGate) {
-    if (tiles(128, 128) < sms) return gemm_launch<1, 64, 1, AMN, BMN, EPI, ACT>(P, pr, products, s);
+  double slices = 0;  // of the longest product
+  for (int i = 0; i < products; ++i) {
+    const double k = double((pr[i].k[0] + kGemmK - 1) / kGemmK + (pr[i].k[1] + kGemmK - 1) / kGemmK);
+    if (k > slices) slices = k;
   }
-  return gemm_launch<1, 128, 1, AMN, BMN, EPI, ACT>(P, pr, products, s);
+  const int64_t m0 = pr[0].m;
+  const double a_rows = AMN || m0 >= kGemmM ? kGemmM : double((m0 + 7) / 8 * 8);
+  // accumulators of 256 x 256 over the pairs; two that share A's rows cost three quarters of their copies
+  const double accs = tiles(256, 256), pairs = sms / 2;
+  const double rounds = std::ceil(accs / pairs);
+  const double shared = kSub == 2 ? (std::floor(accs / pairs / 2) * 2 * 0.75 + (rounds - std::floor(accs / pairs / 2) * 2)) : rounds;
+  double best = shared * slices * std::fmax(256 * kRowNs, 512 * kCycleNs) + kPairNs;
+  int bn = 0, ranks = 0;
+  for (int n : {64, 128}) {
+    const double t = tiles(128, n);
+    for (int r = 1; r <= kSplitMax && r <= slices; r *= 2) {
+      const double per_sm = std::ceil(t * r / sms), part = std::ceil(slices / r);
+      // slices in flight on an SM
+      const double flight = std::fmin(std::fmin(part, double(kSplitStages)) * std::fmin(per_sm, 2.0),
+                                      double(kGemmMaxSmem) / ((a_rows + n) * 128));
+      const double slice = std::fmax(std::fmax((a_rows + n) * kRowNs, 2.0 * n * kCycleNs), kLatencyNs / std::fmax(flight, 1.0));
+      const double ns = per_sm * part * slice + std::ceil(per_sm / 2) * kSplitNs + (r > 1 ? kSumNs : 0.0);
+      if (ns < best) {
+        best = ns;
+        bn = n;
+        ranks = r;
+      }
+    }
+  }
+  if (bn == 64) return gemm_split_launch<64, AMN, BMN, EPI, ACT>(P, pr, products, ranks, s);
+  if (bn == 128) return gemm_split_launch<128, AMN, BMN, EPI, ACT>(P, pr, products, ranks, s);
+  return gemm_launch<2, 256, kSub, AMN, BMN, EPI, ACT>(P, pr, products, s);
 }
 
 }  // namespace prism

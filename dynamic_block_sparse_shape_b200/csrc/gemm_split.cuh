@@ -1,0 +1,262 @@
+// The matrix product of gemm.cuh for few tiles: a cluster of CTAs shares one
+// 128 x BN tile, each CTA multiplying its part of K; the partial sums meet in
+// distributed shared memory.
+//
+// With few tokens or a small layer there are fewer tiles than SMs, and an SM
+// can fetch only so much from L2: a row of 128 bytes takes its copy engine about
+// 1.8 ns (measured: 65 to 72 GB/s per SM, at any clock), so a product is as
+// fast as its operands' rows are spread over SMs. Splitting K needs the sums of
+// the parts: every CTA leaves its fp32 partial tile in its own shared memory
+// (where the operand slices were), and after a cluster barrier CTA r adds
+// column part r of all partial tiles in the order of the ranks (the same bits
+// every time, no atomics, no workspace) and applies the epilogue. Of an operand
+// A with fewer than 128 rows only those (rounded up to 8) are copied: the tensor
+// cores read stale rows beyond them, whose sums nobody reads.
+// A copy comes back after about 1.5 us, so the ring holds as many slices as
+// shared memory takes: all of it when there is a CTA per SM at most, else half,
+// for two CTAs per SM, one's epilogue beside the other's copies.
+#pragma once
+#include "gemm.cuh"
+
+namespace prism {
+
+constexpr int kSplitMax = 8;      // CTAs of a cluster
+constexpr int kSplitStages = 16;  // most slices of a ring
+
+struct SplitArgs {
+  CUtensorMap a[2], b[2];  // as in GemmProduct
+  const __nv_bfloat16* in[2];  // kEpiGateBwd: the saved projections [m, n], contiguous
+  __nv_bfloat16* out[3];
+  int64_t out_ld[3];
+  int m, n;
+  int tiles_m, tiles_n, tile0;
+  int slices0, slices;
+};
+
+struct SplitLaunch {
+  SplitArgs p[kGemmProducts];
+  int products, save;
+  int a_bytes, stages;  // of A's part of a slice, and slices of the ring
+  int* status;
+};
+
+// Shared memory: barriers (1 KB), then the ring. The tensor cores read 16 KB
+// from the start of a slice's A, whatever was copied, so the last slice is
+// followed by room for that. The fp32 partial tile takes the ring's place.
+constexpr int kSplitBars = 1024;
+constexpr int split_pitch(int bn) { return bn + 4; }  // floats between its rows: 16 bytes modulo 32 banks apart
+constexpr int split_smem(int bn, int a_bytes, int stages) {
+  const int ring = stages * (a_bytes + bn * 128) + kGemmM * 128 - a_bytes;
+  const int tile = a_bytes / 128 * split_pitch(bn) * 4;  // the rows that were copied
+  return 1024 + kSplitBars + (ring > tile ? ring : tile);
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+// The sum over the ranks, in their order, of 8 values at `at` (an address of this CTA's partial tile).
+__device__ __forceinline__ void sum_ranks(uint32_t at, int ranks, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  for (int r = 0; r < ranks; ++r) {
+    const uint32_t a = map_shared(at, r);
+    const float4 x = ld_cluster_f4(a), y = ld_cluster_f4(a + 16);
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+template <int BN, bool AMN, bool BMN, int EPI, int ACT>
+__global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __grid_constant__ SplitLaunch P) {
+  constexpr int kPitch = split_pitch(BN);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm);
+  uint64_t* empty = full + kSplitStages;
+  uint64_t* acc_full = empty + kSplitStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_rank());
+  uint32_t ranks_u;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks_u));
+  const int ranks = int(ranks_u);
+  int t = blockIdx.x / ranks, prod = 0;
+  while (prod + 1 < P.products && t >= P.p[prod + 1].tile0) ++prod;
+  const SplitArgs& Q = P.p[prod];
+  t -= Q.tile0;
+  constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;  // output columns
+  const int row0 = (t % Q.tiles_m) * kGemmM, tn = t / Q.tiles_m, col0 = tn * kCols;
+  const int first = int(int64_t(Q.slices) * rank / ranks), last = int(int64_t(Q.slices) * (rank + 1) / ranks);
+  int* status = P.status;
+  sm += kSplitBars;
+  const int stages = P.stages, stage_bytes = P.a_bytes + BN * 128;
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&Q.a[0]);
+    tma_prefetch_desc(&Q.b[0]);
+    if (EPI == kEpiGate) tma_prefetch_desc(&Q.b[1]);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc_cg<1>(tmem_slot, BN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      int st = 0, issued = 0;
+      uint32_t phase = 1;  // of `empty`: a fresh barrier passes
+      for (int kc = first; kc < last; ++kc, ++issued) {
+        ok = mbar_wait_abortable(&empty[st], phase, status, abort_flag);
+        if (!ok) break;
+        const int seg = kc >= Q.slices0;
+        const int k0 = (kc - (seg ? Q.slices0 : 0)) * kGemmK;
+        const uint32_t dst = smem_u32(sm + st * stage_bytes), bar = smem_u32(&full[st]);
+        mbar_arrive_expect_tx(&full[st], stage_bytes);
+        gemm_load<1, AMN>(dst, &Q.a[seg], bar, row0, k0, kGemmM);
+        if constexpr (EPI == kEpiGate) {
+          gemm_load<1, BMN>(dst + P.a_bytes, &Q.b[0], bar, col0, k0, BN / 2);
+          gemm_load<1, BMN>(dst + P.a_bytes + BN / 2 * 128, &Q.b[1], bar, col0, k0, BN / 2);
+        } else {
+          gemm_load<1, BMN>(dst + P.a_bytes, &Q.b[seg], bar, col0, k0, BN);
+        }
+        if (++st == stages) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+        mbar_wait(&full[i % stages], (i / stages) & 1, status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kGemmM, BN, AMN, BMN);
+      constexpr uint64_t kStepA = (AMN ? 2048 : 32) >> 4, kStepB = (BMN ? 2048 : 32) >> 4;
+      bool ok = true;
+      int st = 0;
+      uint32_t phase = 0;
+      for (int kc = first; kc < last; ++kc) {
+        ok = mbar_wait_abortable(&full[st], phase, status, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(sm + st * stage_bytes);
+        const uint64_t da = sdesc_sw128(sa, AMN ? 8192 : 16, 1024);
+        const uint64_t db = sdesc_sw128(sa + P.a_bytes, BMN ? 8192 : 16, 1024);
+#pragma unroll
+        for (int k = 0; k < kGemmK / 16; ++k)
+          mma_bf16<1>(tbase, da + k * kStepA, db + k * kStepB, idesc, (kc > first || k > 0) ? 1u : 0u);
+        mma_commit(&empty[st]);
+        if (++st == stages) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+      mma_commit(acc_full);
+      mbar_wait(acc_full, 0, status);
+    }
+  }
+  __syncwarp();
+  // every copy has landed and every product is complete: the slices' place is free
+  __syncthreads();
+  tc_fence_after();
+  const bool gave_up = *abort_flag;
+  const int rows = min(kGemmM, Q.m - row0);
+  float* part = reinterpret_cast<float*>(sm);
+  if (warp >= 2) {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    if (32 * q < rows) {
+      float* to = part + (32 * q + lane) * kPitch;
+#pragma unroll
+      for (int c = half * 32; c < BN; c += 64) {
+        uint32_t r[32];
+        tmem_ld32(tbase + (uint32_t(q * 32) << 16) + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(to + c + 4 * i) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  // column part `rank` of the tile: 8 columns of a row per thread and step
+  const int vecs = (min(kCols, Q.n - col0) + 7) / 8;  // n is a multiple of 8
+  const int v0 = vecs * rank / ranks, mine = vecs * (rank + 1) / ranks - v0;
+  if (!gave_up && mine > 0) {
+    for (int x = threadIdx.x; x < rows * mine; x += kGemmThreads) {
+      const int r = x / mine, v = v0 + x - r * mine;
+      const uint32_t at = smem_u32(part + r * kPitch + 8 * v);
+      const int64_t row = row0 + r;
+      const int col = col0 + 8 * v;
+      float d[8];
+      sum_ranks(at, ranks, d);
+      if constexpr (EPI == kEpiStore) {
+        *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(d);
+      } else if constexpr (EPI == kEpiGate) {
+        float u[8], h[8];
+        sum_ranks(at + BN / 2 * 4, ranks, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = act_f<ACT>(d[i]) * u[i];
+        *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(h);
+        if (P.save) {
+          *reinterpret_cast<uint4*>(Q.out[1] + row * Q.out_ld[1] + col) = pack8(d);
+          *reinterpret_cast<uint4*>(Q.out[2] + row * Q.out_ld[2] + col) = pack8(u);
+        }
+      } else {
+        float g[8], u[8], dg[8], du[8], h[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(Q.in[0] + row * Q.n + col)), g);
+        unpack8(__ldg(reinterpret_cast<const uint4*>(Q.in[1] + row * Q.n + col)), u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float a, s;
+          act_slope_f<ACT>(g[i], a, s);
+          dg[i] = d[i] * u[i] * s;
+          du[i] = d[i] * a;
+          h[i] = a * u[i];
+        }
+        *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(dg);
+        *reinterpret_cast<uint4*>(Q.out[1] + row * Q.out_ld[1] + col) = pack8(du);
+        if (P.save) *reinterpret_cast<uint4*>(Q.out[2] + row * Q.out_ld[2] + col) = pack8(h);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // nobody reads this CTA's partial tile any more
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<1>(tbase, BN);
+  }
+}
+
+}  // namespace prism
