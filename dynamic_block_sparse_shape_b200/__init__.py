@@ -455,24 +455,25 @@ def _require(ok: bool, what: str, status: int = 1):
 
 class _On:
     """The device of a call's tensors made current, and the stream it runs on: the one given, or that device's
-    current one. Outputs made on another stream than the call's are recorded on it."""
+    current one (`ptr`). Tensors that the call allocates for another stream are recorded on it (`made`)."""
+    __slots__ = ("guard", "stream", "foreign", "ptr")
 
     def __init__(self, tensors, stream, what):
-        first = tensors[0]
-        index = first.get_device()
-        _require(index >= 0, f"{what}: tensors must be on a CUDA device")
+        index = tensors[0].get_device()
         for t in tensors:
-            _require(t.get_device() == index, f"{what}: tensors on different devices")
-        self.index, self.given = index, stream
-        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+            if t.get_device() != index or index < 0:
+                _require(t.get_device() >= 0, f"{what}: tensors must be on a CUDA device")
+                _require(False, f"{what}: tensors on different devices")
+        self.guard = None
+        if index != torch._C._cuda_getDevice():
+            self.guard = torch.cuda.device(index)
+            self.guard.__enter__()
+        own = torch._C._cuda_getCurrentRawStream(index)
+        self.stream = stream
+        self.ptr = own if stream is None else stream.cuda_stream
+        self.foreign = self.ptr != own
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        own = torch.cuda.current_stream(self.index)
-        self.stream = self.given if self.given is not None else own
-        self.foreign = self.given is not None and self.given.cuda_stream != own.cuda_stream
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
         return self
 
     def __exit__(self, *exc):
@@ -480,7 +481,6 @@ class _On:
             self.guard.__exit__(*exc)
 
     def made(self, *tensors):
-        """Tensors that the call allocated, to be used on its stream."""
         if self.foreign:
             for t in tensors:
                 if t is not None:
@@ -527,47 +527,63 @@ class RopeSpec:
 
 def _token_stride(t: torch.Tensor, what: str) -> int:
     """Elements between tokens of a [N, heads, d] tensor with contiguous heads and channels."""
-    _require(t.dim() == 3, f"{what}: [tokens, heads, head_dim] expected")
+    if t.dim() != 3:
+        _require(False, what + ": [tokens, heads, head_dim] expected")
     n, h, d = t.shape
     sn, sh, sd = t.stride()
-    _require((d == 1 or sd == 1) and (h == 1 or sh == d), f"{what}: heads and channels must be contiguous")
+    if (sd != 1 and d != 1) or (sh != d and h != 1):
+        _require(False, what + ": heads and channels must be contiguous")
     return sn if n > 1 else max(sn, h * d)
 
 
+def _like(o, t, what):
+    if o.shape != t.shape or o.dtype != t.dtype or o.device != t.device:
+        _require(False, what + ": an output is not like its input")
+
+
 def _rope(q, k, spec, grid, positions, out, stream, transposed, what):
-    both = (q,) if k is None else (q, k)
-    on = _On(both if positions is None else both + (positions,), stream, what)
     sq = _token_stride(q, what)
     n, hq, d = q.shape
-    hk, sk = 0, 0
     code = _dtype_code(q)
+    tensors = [q]
+    hk, sk, sok, ok, kp, okp = 0, 0, 0, None, None, None
     if k is not None:
         sk = _token_stride(k, what)
-        hk = k.shape[1]
-        _require(k.shape[0] == n and k.shape[2] == d, f"{what}: q and k differ in tokens or head_dim")
-        _require(k.dtype == q.dtype, f"{what}: q and k differ in type", 3)
+        nk, hk, dk = k.shape
+        if nk != n or dk != d:
+            _require(False, what + ": q and k differ in tokens or head_dim")
+        if k.dtype != q.dtype:
+            _require(False, what + ": q and k differ in type", 3)
+        tensors.append(k)
+        kp = k.data_ptr()
+    pp = None
     if positions is not None:
-        _require(positions.dtype == torch.int32, f"{what}: positions must be int32", 3)
-        _require(positions.numel() == n * len(spec.axis_dims) and positions.is_contiguous(),
-                 f"{what}: positions must be contiguous [tokens, axes]")
-    with on:
+        if positions.dtype != torch.int32:
+            _require(False, what + ": positions must be int32", 3)
+        if positions.numel() != n * len(spec.axis_dims) or not positions.is_contiguous():
+            _require(False, what + ": positions must be contiguous [tokens, axes]")
+        tensors.append(positions)
+        pp = positions.data_ptr()
+    with _On(tensors, stream, what) as on:
         if out is None:
-            oq = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-            ok = None if k is None else torch.empty((n, hk, d), dtype=k.dtype, device=k.device)
+            oq = q.new_empty((n, hq, d))
+            soq = hq * d
+            if k is not None:
+                ok = k.new_empty((n, hk, d))
+                sok = hk * d
             on.made(oq, ok)
-            soq, sok = hq * d, hk * d
         else:
             oq, ok = out if k is not None else ((out, None) if torch.is_tensor(out) else (out[0], None))
+            _like(oq, q, what)
             soq = _token_stride(oq, what)
-            sok = 0
-            _require(oq.shape == q.shape and oq.dtype == q.dtype and oq.device == q.device, f"{what}: out is not like q")
             if k is not None:
+                _like(ok, k, what)
                 sok = _token_stride(ok, what)
-                _require(ok.shape == k.shape and ok.dtype == k.dtype and ok.device == k.device,
-                         f"{what}: out is not like k")
+        if k is not None:
+            okp = ok.data_ptr()
         g = None if grid is None else ctypes.byref(_Dim3(*(int(x) for x in grid)))
-        _check(lib().prism_rope(spec._ref, g, _ptr(positions), n, _ptr(q), _ptr(oq), hq, sq, soq, _ptr(k), _ptr(ok),
-                                hk, sk, sok, code, d, transposed, on.ptr), what)
+        _check(lib().prism_rope(spec._ref, g, pp, n, q.data_ptr(), oq.data_ptr(), hq, sq, soq, kp, okp, hk, sk, sok,
+                                code, d, transposed, on.ptr), what)
     return oq, ok
 
 
@@ -589,19 +605,23 @@ def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], spec: RopeSpec, grid=
 _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 
-def _row_stride(t: torch.Tensor, shape, what: str) -> int:
-    """Elements between the rows of a matrix of the given shape with contiguous rows."""
-    _require(t.dim() == 2 and (shape is None or tuple(t.shape) == shape), f"{what} must be {list(shape or 'mn')}")
-    _require(t.shape[1] == 1 or t.stride(1) == 1, f"{what}: rows must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), -(-t.shape[1] // 8) * 8)
+def _row_stride(t: torch.Tensor, rows, cols, what: str, name: str) -> int:
+    """Elements between the rows of a [rows, cols] matrix with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        _require(False, f"{what}: {name} must be [{rows}, {cols}]")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols != 1:
+        _require(False, f"{what}: the rows of {name} must be contiguous")
+    return s0 if rows > 1 else max(s0, -(-cols // 8) * 8)
 
 
 def _ffn_weights(w_gate, w_up, w_down, what):
-    _require(w_gate.dim() == 2, f"{what}: w_gate must be [f, d]")
+    if w_gate.dim() != 2:
+        _require(False, what + ": w_gate must be [f, d]")
     f, d = w_gate.shape
-    sg, su = _row_stride(w_gate, None, f"{what}: w_gate"), _row_stride(w_up, (f, d), f"{what}: w_up")
-    sd = _row_stride(w_down, (d, f), f"{what}: w_down")
-    return _FfnWeights(w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), sg, su, sd, d, f), d, f
+    return _FfnWeights(w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+                       _row_stride(w_gate, f, d, what, "w_gate"), _row_stride(w_up, f, d, what, "w_up"),
+                       _row_stride(w_down, d, f, what, "w_down"), d, f), d, f
 
 
 def _ffn_workspace(ws, m, f, backward, device):
@@ -611,8 +631,10 @@ def _ffn_workspace(ws, m, f, backward, device):
 
 
 def _same_type(tensors, what):
+    kind = tensors[0].dtype
     for t in tensors:
-        _require(t.dtype == tensors[0].dtype, f"{what}: tensors of different types", 3)
+        if t.dtype != kind:
+            _require(False, what + ": tensors of different types", 3)
     return _dtype_code(tensors[0])
 
 
@@ -623,20 +645,28 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
     act: "silu", "gelu", "gelu_tanh" or "relu". Returns (y, gate, up): with ``save`` the projections [m, f] that
     ``gated_ffn_bwd`` needs, else None. out: where y goes."""
     what = "prism_gated_ffn_fwd"
-    _require(act in _ACT, f"{what}: act {act!r}")
-    code = _same_type((x, w_gate, w_up, w_down) + (() if out is None else (out,)), what)
+    if act not in _ACT:
+        _require(False, f"{what}: act {act!r}")
+    every = (x, w_gate, w_up, w_down) if out is None else (x, w_gate, w_up, w_down, out)
+    code = _same_type(every, what)
     w, d, f = _ffn_weights(w_gate, w_up, w_down, what)
-    sx = _row_stride(x, (x.shape[0], d), f"{what}: x")
-    m = x.shape[0]
-    with _On((x, w_gate, w_up, w_down) + (() if out is None else (out,)), stream, what) as on:
+    m = x.shape[0] if x.dim() else 0
+    sx = _row_stride(x, m, d, what, "x")
+    with _On(every, stream, what) as on:
         ws = _ffn_workspace(ws, m, f, 0, x.device)
-        y = torch.empty((m, d), dtype=x.dtype, device=x.device) if out is None else out
-        gate = torch.empty((m, f), dtype=x.dtype, device=x.device) if save else None
-        up = torch.empty((m, f), dtype=x.dtype, device=x.device) if save else None
+        y, gate, up, gp, upp = out, None, None, None, None
+        if out is None:
+            y = x.new_empty((m, d))
+            sy = d
+        else:
+            sy = _row_stride(y, m, d, what, "out")
+        if save:
+            gate = x.new_empty((m, f))
+            up = x.new_empty((m, f))
+            gp, upp = gate.data_ptr(), up.data_ptr()
         on.made(y, gate, up, ws.buf)
-        _check(lib().prism_gated_ffn_fwd(ctypes.byref(w), m, _ACT[act], code, _ptr(x), sx, _ptr(y),
-                                         _row_stride(y, (m, d), f"{what}: out"), _ptr(gate), _ptr(up), ws.ptr,
-                                         ws.nbytes, on.ptr), what)
+        _check(lib().prism_gated_ffn_fwd(ctypes.byref(w), m, _ACT[act], code, x.data_ptr(), sx, y.data_ptr(), sy, gp, upp,
+                                         ws.ptr, ws.nbytes, on.ptr), what)
     return y, gate, up
 
 
@@ -646,23 +676,31 @@ def gated_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up:
     """Gradient of ``gated_ffn_fwd`` at its saved projections: (dx, dw_gate, dw_up, dw_down); without ``need_dx`` or
     ``need_dw`` None in their places."""
     what = "prism_gated_ffn_bwd"
-    _require(act in _ACT, f"{what}: act {act!r}")
+    if act not in _ACT:
+        _require(False, f"{what}: act {act!r}")
     every = (dy, x, w_gate, w_up, w_down, gate, up)
     code = _same_type(every, what)
     w, d, f = _ffn_weights(w_gate, w_up, w_down, what)
-    m = x.shape[0]
-    sx, sdy = _row_stride(x, (m, d), f"{what}: x"), _row_stride(dy, (m, d), f"{what}: dy")
+    m = x.shape[0] if x.dim() else 0
+    sx, sdy = _row_stride(x, m, d, what, "x"), _row_stride(dy, m, d, what, "dy")
     for t in (gate, up):
-        _require(tuple(t.shape) == (m, f) and t.is_contiguous(), f"{what}: gate and up must be contiguous [m, f]")
+        if t.shape != (m, f) or not t.is_contiguous():
+            _require(False, what + ": gate and up must be contiguous [m, f]")
     with _On(every, stream, what) as on:
         ws = _ffn_workspace(ws, m, f, 1, x.device)
-        new = lambda *s: torch.empty(s, dtype=x.dtype, device=x.device)  # noqa: E731
-        dx = new(m, d) if need_dx else None
-        dwg, dwu, dwd = (new(f, d), new(f, d), new(d, f)) if need_dw else (None, None, None)
+        dx = dwg = dwu = dwd = xp = gp = upp = dp = None
+        if need_dx:
+            dx = x.new_empty((m, d))
+            xp = dx.data_ptr()
+        if need_dw:
+            dwg = x.new_empty((f, d))
+            dwu = x.new_empty((f, d))
+            dwd = x.new_empty((d, f))
+            gp, upp, dp = dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()
         on.made(dx, dwg, dwu, dwd, ws.buf)
-        _check(lib().prism_gated_ffn_bwd(ctypes.byref(w), m, _ACT[act], code, _ptr(dy), sdy, _ptr(x), sx, _ptr(gate),
-                                         _ptr(up), _ptr(dx), d, _ptr(dwg), _ptr(dwu), _ptr(dwd), ws.ptr, ws.nbytes,
-                                         on.ptr), what)
+        _check(lib().prism_gated_ffn_bwd(ctypes.byref(w), m, _ACT[act], code, dy.data_ptr(), sdy, x.data_ptr(), sx,
+                                         gate.data_ptr(), up.data_ptr(), xp, d, gp, upp, dp, ws.ptr, ws.nbytes, on.ptr),
+               what)
     return dx, dwg, dwu, dwd
 
 
@@ -707,9 +745,8 @@ def _grad_list(grads, out=None) -> GradList:
 def _norm_call(grads, ws, device, stream, what):
     device = grads.device or torch.device(device)
     norm = torch.empty((), dtype=torch.float32, device=device)
-    on = _On(grads.grads[:1] + [norm], stream, what)
     ws = (ws or Workspace(device)).ensure(grads.workspace_bytes)
-    return norm, on, ws
+    return norm, _On((norm,), stream, what), ws
 
 
 def grad_norm(grads, ord=2, ws: Optional[Workspace] = None, device="cuda", stream=None) -> torch.Tensor:
@@ -720,7 +757,7 @@ def grad_norm(grads, ord=2, ws: Optional[Workspace] = None, device="cuda", strea
     norm, on, ws = _norm_call(grads, ws, device, stream, "prism_grad_norm")
     with on:
         on.made(norm, ws.buf)
-        _check(lib().prism_grad_norm(grads._c, grads.n, _NORM[ord], _ptr(norm), ws.ptr, ws.nbytes, on.ptr),
+        _check(lib().prism_grad_norm(grads._c, grads.n, _NORM[ord], norm.data_ptr(), ws.ptr, ws.nbytes, on.ptr),
                "prism_grad_norm")
     return norm
 
@@ -739,11 +776,12 @@ def clip_grad_norm(grads, max_norm: float, ord=2, out=None, eps: float = 1e-6, w
                    device="cuda", stream=None) -> torch.Tensor:
     """``grad_norm`` and ``scale_grads`` of a list of gradients or a ``GradList``: returns the norm before clipping."""
     grads = _grad_list(grads, out)
-    _require(ord in _NORM, f"prism_grad_clip: ord {ord!r}")
+    if ord not in _NORM:
+        _require(False, f"prism_grad_clip: ord {ord!r}")
     norm, on, ws = _norm_call(grads, ws, device, stream, "prism_grad_clip")
     with on:
         on.made(norm, ws.buf)
-        _check(lib().prism_grad_clip(grads._c, grads.n, _NORM[ord], float(max_norm), float(eps), _ptr(norm), ws.ptr,
+        _check(lib().prism_grad_clip(grads._c, grads.n, _NORM[ord], float(max_norm), float(eps), norm.data_ptr(), ws.ptr,
                                      ws.nbytes, on.ptr), "prism_grad_clip")
     return norm
 

@@ -192,14 +192,15 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrives once on `bar` (of both CTAs of a pair) when this thread's products so far are complete.
+// Arrives once on `bar` (of both CTAs of a pair; `leader`: its even rank in the
+// cluster) when this thread's products so far are complete.
 template <int CG>
-__device__ __forceinline__ void mma_commit_all(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit_all(uint64_t* bar, uint32_t leader = 0) {
   if constexpr (CG == 2)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"(uint16_t(3))
+        "h"(uint16_t(3u << leader))
         : "memory");
   else
     mma_commit(bar);

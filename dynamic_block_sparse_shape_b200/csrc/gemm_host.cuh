@@ -112,15 +112,15 @@ prism_status gemm_launch(GemmArgs& P, const GemmProblem* pr, int products, cudaS
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, P));
 }
 
-template <int BN, bool AMN, bool BMN, int EPI, int ACT>
-prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int products, int ranks, cudaStream_t s) {
+template <int CG, int BN, bool AMN, bool BMN, int EPI, int ACT>
+prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int products, int parts, cudaStream_t s) {
   constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;
   SplitLaunch A;
   std::memset(&A, 0, sizeof(A));
   A.products = products;
   A.save = P.save;
   A.status = P.status;
-  const int a_rows = AMN || pr[0].m >= kGemmM ? kGemmM : int(pr[0].m + 7) / 8 * 8;
+  const int a_rows = AMN || CG == 2 || pr[0].m >= kGemmM ? kGemmM : int(pr[0].m + 7) / 8 * 8;
   A.a_bytes = a_rows * 128;
   int64_t tiles = 0, slices = 0;
   for (int i = 0; i < products; ++i) {
@@ -128,7 +128,7 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
     const GemmProblem& R = pr[i];
     Q.m = int(R.m);
     Q.n = int(R.n);
-    Q.tiles_m = int((R.m + kGemmM - 1) / kGemmM);
+    Q.tiles_m = int((R.m + CG * kGemmM - 1) / (CG * kGemmM));
     Q.tiles_n = int((R.n + kCols - 1) / kCols);
     Q.tile0 = int(tiles);
     tiles += int64_t(Q.tiles_m) * Q.tiles_n;
@@ -139,7 +139,7 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
     for (int g = 0; g < 2 && st == PRISM_OK; ++g) {
       if (R.a[g].base) st = gemm_operand_map(&Q.a[g], R.a[g], AMN, R.m, R.k[g], a_rows);
       const int64_t kb = EPI == kEpiGate ? R.k[0] : R.k[g];
-      if (R.b[g].base && st == PRISM_OK) st = gemm_operand_map(&Q.b[g], R.b[g], BMN, R.n, kb, kCols);
+      if (R.b[g].base && st == PRISM_OK) st = gemm_operand_map(&Q.b[g], R.b[g], BMN, R.n, kb, EPI == kEpiGate ? BN / 2 : BN / CG);
       Q.in[g] = static_cast<const __nv_bfloat16*>(R.in[g]);
     }
     if (st != PRISM_OK) return st;
@@ -148,13 +148,14 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
       Q.out_ld[g] = R.out[g].ld;
     }
   }
+  const int ranks = CG * parts;
   if (tiles * ranks >= (int64_t(1) << 31)) return PRISM_ERR_UNSUPPORTED;
   // a ring of all of an SM's shared memory, or two of half of it
-  const int room = tiles * ranks <= device_sm_count() ? kGemmMaxSmem : 113 * 1024;
-  A.stages = int(std::min<int64_t>(kSplitStages, (slices + ranks - 1) / ranks));
-  while (A.stages > 1 && split_smem(BN, A.a_bytes, A.stages) > room) --A.stages;
-  const int smem = split_smem(BN, A.a_bytes, A.stages);
-  auto kernel = gemm_split_kernel<BN, AMN, BMN, EPI, ACT>;
+  const int room = CG == 2 || (tiles * ranks <= device_sm_count() && ranks < kSplitMax) ? kGemmMaxSmem : 113 * 1024;
+  A.stages = int(std::min<int64_t>(kSplitStages, (slices + parts - 1) / parts));
+  while (A.stages > 1 && split_smem(CG, BN, A.a_bytes, A.stages) > room) --A.stages;
+  const int smem = split_smem(CG, BN, A.a_bytes, A.stages);
+  auto kernel = gemm_split_kernel<CG, BN, AMN, BMN, EPI, ACT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmMaxSmem) != cudaSuccess)
     return PRISM_ERR_CUDA;
   cudaLaunchConfig_t cfg;
@@ -172,58 +173,77 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, A));
 }
 
-// Time of a product in ns by what it is made of: an SM's copy engine takes
-// kRowNs per 128-byte row, a slice's products their tensor cycles, and a round
-// of tiles its fill and epilogue.
-constexpr double kRowNs = 1.8, kLatencyNs = 1500.0, kCycleNs = 1.0 / 1.8, kPairNs = 4000.0, kSplitNs = 3000.0, kSumNs = 1000.0;
+// Time of a product in ns by what it is made of (measured on products of 16 to
+// 2000 rows): an SM fetches kRate bytes per ns from L2, rows that do not start
+// on 128-byte borders count kRagged times; a slice takes at least its tensor
+// cycles and kSliceNs, and a ring's slices come back after kLatencyNs; a tile's
+// fill and epilogue, and the joining of parts.
+constexpr double kRate = 90.0, kRagged = 1.3, kLatencyNs = 1500.0, kSliceNs = 250.0, kCycleNs = 1.0 / 1.7,
+                 kTileNs = 6000.0, kJoinNs = 1500.0, kJoinRate = 60.0;
 
-// The kernel and tiles for a product: pairs of CTAs for many tiles (SUB = 2
-// shares A's rows; the gradient of the gate has the longest epilogue and
-// alternates its accumulators to hide it), K split over a cluster for few. The
-// times decide, from measured rates; what they are off by shows only where two
-// choices are close.
-template <bool AMN, bool BMN, int EPI, int ACT>
-prism_status gemm(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s) {
+struct GemmChoice {
+  int cg, bn, parts;  // bn = 0: the pair kernel of gemm.cuh
+};
+
+// The kernel and tiles for products of m x n rows each (n: columns of the
+// accumulator): the choice of least time by the figures above; what they are
+// off by shows only where two choices are close. `sub`: accumulators of a tile
+// of the pair kernel.
+inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, int64_t slices, bool a_mn, int sub,
+                              bool ragged) {
   const int sms = device_sm_count();
-  constexpr int kHalf = EPI == kEpiGate ? 2 : 1;
-  constexpr int kSub = EPI == kEpiGateBwd ? 1 : 2;
   auto tiles = [&](int64_t rows, int64_t cols) {
     double t = 0;
-    for (int i = 0; i < products; ++i) t += double((pr[i].m + rows - 1) / rows) * double((pr[i].n * kHalf + cols - 1) / cols);
+    for (int i = 0; i < products; ++i) t += double((m[i] + rows - 1) / rows) * double((n[i] + cols - 1) / cols);
     return t;
   };
-  double slices = 0;  // of the longest product
-  for (int i = 0; i < products; ++i) {
-    const double k = double((pr[i].k[0] + kGemmK - 1) / kGemmK + (pr[i].k[1] + kGemmK - 1) / kGemmK);
-    if (k > slices) slices = k;
-  }
-  const int64_t m0 = pr[0].m;
-  const double a_rows = AMN || m0 >= kGemmM ? kGemmM : double((m0 + 7) / 8 * 8);
-  // accumulators of 256 x 256 over the pairs; two that share A's rows cost three quarters of their copies
-  const double accs = tiles(256, 256), pairs = sms / 2;
-  const double rounds = std::ceil(accs / pairs);
-  const double shared = kSub == 2 ? (std::floor(accs / pairs / 2) * 2 * 0.75 + (rounds - std::floor(accs / pairs / 2) * 2)) : rounds;
-  double best = shared * slices * std::fmax(256 * kRowNs, 512 * kCycleNs) + kPairNs;
-  int bn = 0, ranks = 0;
-  for (int n : {64, 128}) {
-    const double t = tiles(128, n);
-    for (int r = 1; r <= kSplitMax && r <= slices; r *= 2) {
-      const double per_sm = std::ceil(t * r / sms), part = std::ceil(slices / r);
-      // slices in flight on an SM
-      const double flight = std::fmin(std::fmin(part, double(kSplitStages)) * std::fmin(per_sm, 2.0),
-                                      double(kGemmMaxSmem) / ((a_rows + n) * 128));
-      const double slice = std::fmax(std::fmax((a_rows + n) * kRowNs, 2.0 * n * kCycleNs), kLatencyNs / std::fmax(flight, 1.0));
-      const double ns = per_sm * part * slice + std::ceil(per_sm / 2) * kSplitNs + (r > 1 ? kSumNs : 0.0);
+  const double rate = ragged ? kRate / kRagged : kRate, k = double(slices);
+  // pairs: rounds of tiles, the last one of single accumulators when it is less than half full
+  const double pairs = sms / 2, accs = tiles(256, 256);
+  const double whole = std::floor(accs / sub / pairs), rest = accs / sub - whole * pairs;
+  const double one = std::fmax(32768.0 / rate, 512 * kCycleNs);
+  const double both = sub == 1 ? one : std::fmax(49152.0 / rate, 1024 * kCycleNs);
+  double best = k * (whole * both + (rest > 0 ? (rest * 2 <= pairs ? one : both) : 0.0)) + kTileNs;
+  GemmChoice c = {2, 0, 1};
+  const GemmChoice tries[] = {{1, 64, 8}, {1, 128, 4}, {2, 256, 4}};  // with the most parts
+  for (const GemmChoice& t : tries) {
+    const int rows_a = a_mn || t.cg == 2 || m[0] >= kGemmM ? kGemmM : int(m[0] + 7) / 8 * 8;
+    const double bytes = (rows_a + t.bn / t.cg) * 128.0;
+    for (int parts = 1; parts <= t.parts && parts <= slices; parts *= 2) {
+      const double ctas = tiles(kGemmM * t.cg, t.bn) * t.cg * parts, per_sm = std::ceil(ctas / sms);
+      const double mine = std::ceil(k / parts);
+      const double flight = std::fmin(std::fmin(mine, double(kSplitStages)) * (t.cg == 2 ? 1.0 : std::fmin(per_sm, 2.0)),
+                                      kGemmMaxSmem / bytes);
+      const double slice = std::fmax(std::fmax(bytes / rate, kSliceNs), kLatencyNs / std::fmax(flight, 1.0));
+      const double rounds = t.cg == 2 ? per_sm : std::ceil(per_sm / 2);
+      const double join = parts > 1 ? rounds * kJoinNs + per_sm * rows_a * t.bn * 4.0 / kJoinRate : 0.0;
+      const double ns = per_sm * mine * slice + rounds * kTileNs + join;
       if (ns < best) {
         best = ns;
-        bn = n;
-        ranks = r;
+        c = {t.cg, t.bn, parts};
       }
     }
   }
-  if (bn == 64) return gemm_split_launch<64, AMN, BMN, EPI, ACT>(P, pr, products, ranks, s);
-  if (bn == 128) return gemm_split_launch<128, AMN, BMN, EPI, ACT>(P, pr, products, ranks, s);
-  return gemm_launch<2, 256, kSub, AMN, BMN, EPI, ACT>(P, pr, products, s);
+  return c;
+}
+
+template <bool AMN, bool BMN, int EPI, int ACT>
+prism_status gemm(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s) {
+  // the gradient of the gate has the longest epilogue: it alternates its accumulators to hide it
+  constexpr int kSub = EPI == kEpiGateBwd ? 1 : 2;
+  int64_t m[kGemmProducts], n[kGemmProducts], slices = 0;
+  bool ragged = false;
+  for (int i = 0; i < products; ++i) {
+    m[i] = pr[i].m;
+    n[i] = pr[i].n * (EPI == kEpiGate ? 2 : 1);
+    slices = std::max(slices, (pr[i].k[0] + kGemmK - 1) / kGemmK + (pr[i].k[1] + kGemmK - 1) / kGemmK);
+    ragged = ragged || pr[i].a[0].ld % 64 || pr[i].b[0].ld % 64;
+  }
+  const GemmChoice c = gemm_choice(m, n, products, slices, AMN, kSub, ragged);
+  if (c.bn == 0) return gemm_launch<2, 256, kSub, AMN, BMN, EPI, ACT>(P, pr, products, s);
+  if (c.cg == 1 && c.bn == 64) return gemm_split_launch<1, 64, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);
+  if (c.cg == 1) return gemm_split_launch<1, 128, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);
+  return gemm_split_launch<2, 256, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);
 }
 
 }  // namespace prism

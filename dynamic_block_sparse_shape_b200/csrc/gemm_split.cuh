@@ -1,14 +1,13 @@
-// The matrix product of gemm.cuh for few tiles: a cluster of CTAs shares one
-// 128 x BN tile, each CTA multiplying its part of K; the partial sums meet in
-// distributed shared memory.
+// The matrix product of gemm.cuh for few tiles: a cluster shares one tile (128 x
+// BN of single CTAs, 256 x BN of pairs), each CTA or pair multiplying its part
+// of K; the partial sums meet in distributed shared memory.
 //
 // With few tokens or a small layer there are fewer tiles than SMs, and an SM
-// can fetch only so much from L2: a row of 128 bytes takes its copy engine about
-// 1.8 ns (measured: 65 to 72 GB/s per SM, at any clock), so a product is as
-// fast as its operands' rows are spread over SMs. Splitting K needs the sums of
-// the parts: every CTA leaves its fp32 partial tile in its own shared memory
-// (where the operand slices were), and after a cluster barrier CTA r adds
-// column part r of all partial tiles in the order of the ranks (the same bits
+// fetches at most some 90 GB/s from L2 (measured), so a product is as fast as
+// its operands' bytes are spread over SMs. Splitting K needs the sums of the
+// parts: every CTA leaves its fp32 partial tile in its own shared memory (where
+// the operand slices were), and after a cluster barrier part r of the CTAs adds
+// column part r of all partial tiles in the order of the parts (the same bits
 // every time, no atomics, no workspace) and applies the epilogue. Of an operand
 // A with fewer than 128 rows only those (rounded up to 8) are copied: the tensor
 // cores read stale rows beyond them, whose sums nobody reads.
@@ -45,9 +44,9 @@ struct SplitLaunch {
 // followed by room for that. The fp32 partial tile takes the ring's place.
 constexpr int kSplitBars = 1024;
 constexpr int split_pitch(int bn) { return bn + 4; }  // floats between its rows: 16 bytes modulo 32 banks apart
-constexpr int split_smem(int bn, int a_bytes, int stages) {
-  const int ring = stages * (a_bytes + bn * 128) + kGemmM * 128 - a_bytes;
-  const int tile = a_bytes / 128 * split_pitch(bn) * 4;  // the rows that were copied
+constexpr int split_smem(int cg, int bn, int a_bytes, int stages) {
+  const int ring = stages * (a_bytes + bn / cg * 128) + kGemmM * 128 - a_bytes;
+  const int tile = (a_bytes / 128 + 31) / 32 * 32 * split_pitch(bn) * 4;  // a warp's 32 rows at a time
   return 1024 + kSplitBars + (ring > tile ? ring : tile);
 }
 
@@ -59,15 +58,27 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-// The sum over the ranks, in their order, of 8 values at `at` (an address of this CTA's partial tile).
-__device__ __forceinline__ void sum_ranks(uint32_t at, int ranks, float* v) {
+// The sum over the parts, in their order, of 8 values at `at` (an address of
+// this CTA's partial tile): four parts' loads in flight at a time.
+template <int CG>
+__device__ __forceinline__ void sum_parts(uint32_t at, int parts, uint32_t cta, float* v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  for (int r = 0; r < ranks; ++r) {
-    const uint32_t a = map_shared(at, r);
-    const float4 x = ld_cluster_f4(a), y = ld_cluster_f4(a + 16);
-    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+  for (int p0 = 0; p0 < parts; p0 += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      if (p0 + p < parts) {
+        const uint32_t a = map_shared(at, CG * (p0 + p) + cta);
+        x[p] = ld_cluster_f4(a);
+        y[p] = ld_cluster_f4(a + 16);
+      }
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      if (p0 + p < parts) {
+        v[0] += x[p].x; v[1] += x[p].y; v[2] += x[p].z; v[3] += x[p].w;
+        v[4] += y[p].x; v[5] += y[p].y; v[6] += y[p].z; v[7] += y[p].w;
+      }
   }
 }
 
@@ -83,8 +94,8 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* v) {
   }
 }
 
-template <int BN, bool AMN, bool BMN, int EPI, int ACT>
-__global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __grid_constant__ SplitLaunch P) {
+template <int CG, int BN, bool AMN, bool BMN, int EPI, int ACT>
+__global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kernel(const __grid_constant__ SplitLaunch P) {
   constexpr int kPitch = split_pitch(BN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -94,20 +105,20 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = int(cluster_rank());
-  uint32_t ranks_u;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks_u));
-  const int ranks = int(ranks_u);
+  const uint32_t rank = cluster_rank(), cta = CG == 2 ? rank & 1 : 0, leader = rank - cta;
+  uint32_t ranks;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int part_of = int(rank) / CG, parts = int(ranks) / CG;  // of K
   int t = blockIdx.x / ranks, prod = 0;
   while (prod + 1 < P.products && t >= P.p[prod + 1].tile0) ++prod;
   const SplitArgs& Q = P.p[prod];
   t -= Q.tile0;
   constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;  // output columns
-  const int row0 = (t % Q.tiles_m) * kGemmM, tn = t / Q.tiles_m, col0 = tn * kCols;
-  const int first = int(int64_t(Q.slices) * rank / ranks), last = int(int64_t(Q.slices) * (rank + 1) / ranks);
+  const int row0 = ((t % Q.tiles_m) * CG + int(cta)) * kGemmM, tn = t / Q.tiles_m, col0 = tn * kCols;
+  const int first = int(int64_t(Q.slices) * part_of / parts), last = int(int64_t(Q.slices) * (part_of + 1) / parts);
   int* status = P.status;
   sm += kSplitBars;
-  const int stages = P.stages, stage_bytes = P.a_bytes + BN * 128;
+  const int stages = P.stages, stage_bytes = P.a_bytes + BN / CG * 128;
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&Q.a[0]);
     tma_prefetch_desc(&Q.b[0]);
@@ -122,9 +133,10 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __gri
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc_cg<1>(tmem_slot, BN);
+  if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, BN);
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
@@ -141,26 +153,32 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __gri
         if (!ok) break;
         const int seg = kc >= Q.slices0;
         const int k0 = (kc - (seg ? Q.slices0 : 0)) * kGemmK;
-        const uint32_t dst = smem_u32(sm + st * stage_bytes), bar = smem_u32(&full[st]);
-        mbar_arrive_expect_tx(&full[st], stage_bytes);
-        gemm_load<1, AMN>(dst, &Q.a[seg], bar, row0, k0, kGemmM);
-        if constexpr (EPI == kEpiGate) {
-          gemm_load<1, BMN>(dst + P.a_bytes, &Q.b[0], bar, col0, k0, BN / 2);
-          gemm_load<1, BMN>(dst + P.a_bytes + BN / 2 * 128, &Q.b[1], bar, col0, k0, BN / 2);
+        const uint32_t dst = smem_u32(sm + st * stage_bytes);
+        uint32_t bar = smem_u32(&full[st]);
+        if constexpr (CG == 2) bar = map_shared(bar, leader);
+        if (cta == 0) mbar_arrive_expect_tx(&full[st], CG * stage_bytes);
+        gemm_load<CG, AMN>(dst, &Q.a[seg], bar, row0, k0, kGemmM);
+        if constexpr (EPI == kEpiGate && CG == 2) {
+          gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[cta], bar, col0, k0, BN / 2);
+        } else if constexpr (EPI == kEpiGate) {
+          gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[0], bar, col0, k0, BN / 2);
+          gemm_load<CG, BMN>(dst + P.a_bytes + BN / 2 * 128, &Q.b[1], bar, col0, k0, BN / 2);
         } else {
-          gemm_load<1, BMN>(dst + P.a_bytes, &Q.b[seg], bar, col0, k0, BN);
+          gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[seg], bar, col0 + int(cta) * (BN / CG), k0, BN / CG);
         }
         if (++st == stages) {
           st = 0;
           phase ^= 1;
         }
       }
-      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-        mbar_wait(&full[i % stages], (i / stages) & 1, status);
+      // the leader's barriers count both CTAs' copies
+      if (cta == 0)
+        for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+          mbar_wait(&full[i % stages], (i / stages) & 1, status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kGemmM, BN, AMN, BMN);
+    if (lane == 0 && cta == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kGemmM * CG, BN, AMN, BMN);
       constexpr uint64_t kStepA = (AMN ? 2048 : 32) >> 4, kStepB = (BMN ? 2048 : 32) >> 4;
       bool ok = true;
       int st = 0;
@@ -174,18 +192,28 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __gri
         const uint64_t db = sdesc_sw128(sa + P.a_bytes, BMN ? 8192 : 16, 1024);
 #pragma unroll
         for (int k = 0; k < kGemmK / 16; ++k)
-          mma_bf16<1>(tbase, da + k * kStepA, db + k * kStepB, idesc, (kc > first || k > 0) ? 1u : 0u);
-        mma_commit(&empty[st]);
+          mma_bf16<CG>(tbase, da + k * kStepA, db + k * kStepB, idesc, (kc > first || k > 0) ? 1u : 0u);
+        mma_commit_all<CG>(&empty[st], leader);
         if (++st == stages) {
           st = 0;
           phase ^= 1;
         }
       }
-      mma_commit(acc_full);
-      mbar_wait(acc_full, 0, status);
+      mma_commit_all<CG>(acc_full, leader);
     }
+    // also in the pair's other CTA, which issues nothing
+    if (lane == 0) mbar_wait_abortable(acc_full, 0, status, abort_flag);
   }
   __syncwarp();
+  if constexpr (CG == 2) {
+    // a pair that gave up may leave copies of the other CTA on their way: let them land
+    if (*abort_flag) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000) {
+      }
+      __syncwarp();
+    }
+  }
   // every copy has landed and every product is complete: the slices' place is free
   __syncthreads();
   tc_fence_after();
@@ -210,9 +238,9 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __gri
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();
-  // column part `rank` of the tile: 8 columns of a row per thread and step
+  // column part `part_of` of the tile: 8 columns of a row per thread and step
   const int vecs = (min(kCols, Q.n - col0) + 7) / 8;  // n is a multiple of 8
-  const int v0 = vecs * rank / ranks, mine = vecs * (rank + 1) / ranks - v0;
+  const int v0 = vecs * part_of / parts, mine = vecs * (part_of + 1) / parts - v0;
   if (!gave_up && mine > 0) {
     for (int x = threadIdx.x; x < rows * mine; x += kGemmThreads) {
       const int r = x / mine, v = v0 + x - r * mine;
@@ -220,12 +248,12 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __gri
       const int64_t row = row0 + r;
       const int col = col0 + 8 * v;
       float d[8];
-      sum_ranks(at, ranks, d);
+      sum_parts<CG>(at, parts, cta, d);
       if constexpr (EPI == kEpiStore) {
         *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(d);
       } else if constexpr (EPI == kEpiGate) {
         float u[8], h[8];
-        sum_ranks(at + BN / 2 * 4, ranks, u);
+        sum_parts<CG>(at + BN / 2 * 4, parts, cta, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = act_f<ACT>(d[i]) * u[i];
         *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(h);
@@ -255,7 +283,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) gemm_split_kernel(const __gri
   cluster_sync_all();  // nobody reads this CTA's partial tile any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_cg<1>(tbase, BN);
+    tmem_dealloc_cg<CG>(tbase, BN);
   }
 }
 
