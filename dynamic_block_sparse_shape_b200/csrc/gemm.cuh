@@ -22,7 +22,7 @@
 // Roles of a CTA's ten warps: 0 issues the copies into a ring of slices; 1
 // owns the tensor memory and issues the products (of the pair: the leader's);
 // 2..9 read the accumulators (a thread per row, two warps per row alternating
-// over 32-column pieces), apply the epilogue and store 32 x 32 pieces by TMA.
+// over pieces of columns), apply the epilogue and store the pieces by TMA.
 // SUB = 1: the two accumulators alternate, the epilogue of a tile runs beside
 // the products of the next. SUB = 2: the next tile's first slices are
 // multiplied into the first accumulator while the second is still being read.
@@ -39,9 +39,7 @@ constexpr int kGemmM = 128;    // rows of A per CTA
 constexpr int kGemmK = 64;     // a slice of K: one 128-byte swizzle row
 constexpr int kGemmEpiWarps = 8;
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
-constexpr int kGemmPiece = 32;                      // columns of an epilogue piece
-constexpr int kGemmPieceBytes = 32 * kGemmPiece * 2;  // 32 rows x 32 bf16, 64-byte swizzle
-constexpr int kGemmOutPieces = 2;                   // staging ring of an epilogue warp
+constexpr int kGemmOutBytes = 4096;  // staging of an epilogue warp
 // tile rows per group: 4 to 20 measured on [16384, 4096] x [11264, 4096], 12 best by 1 to 3 %
 constexpr int kGemmGroupM = 12;
 constexpr int kGemmProducts = 3;
@@ -66,7 +64,7 @@ struct GemmProduct {
 
 struct GemmArgs {
   GemmProduct p[kGemmProducts];
-  CUtensorMap in[2];  // kEpiGateBwd: the saved projections, 32 x 32 pieces
+  CUtensorMap in[2];  // kEpiGateBwd: the saved projections
   int products;
   int whole, units;   // tiles taken whole; these and the halves of the others
   int save;
@@ -74,13 +72,27 @@ struct GemmArgs {
   int* status;
 };
 
+// An epilogue piece is 32 rows x COLS bf16 values in swizzled rows: 64 columns
+// (rows of 128 bytes: the copy engine's cost is by the row) where a warp stages
+// one piece, 32 (rows of 64 bytes) where the gradient of the gate stages two
+// and has two more coming in.
+template <int COLS>
+struct Piece {
+  static constexpr int kBytes = 32 * COLS * 2, kSlots = kGemmOutBytes / kBytes, kChunks = COLS / 8;
+  // byte offset of 16-byte chunk `chunk` of row `row`
+  static __device__ __forceinline__ uint32_t offset(uint32_t row, uint32_t chunk) {
+    return COLS == 64 ? sw128_offset(row, chunk) : row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+  }
+};
+constexpr int gemm_piece_cols(int epi) { return epi == kEpiGateBwd ? 32 : 64; }
+
 template <int CG, int BN, int SUB, int EPI>
 struct GemmLayout {
   static constexpr int kA = kGemmM * 128;
   static constexpr int kB = BN / CG * 128;
   static constexpr int kStage = kA + SUB * kB;
-  static constexpr int kOutBytes = kGemmEpiWarps * kGemmOutPieces * kGemmPieceBytes;
-  static constexpr int kInBytes = EPI == kEpiGateBwd ? kGemmEpiWarps * 2 * kGemmPieceBytes : 0;
+  static constexpr int kOutBytes = kGemmEpiWarps * kGemmOutBytes;
+  static constexpr int kInBytes = EPI == kEpiGateBwd ? kGemmEpiWarps * 2 * Piece<32>::kBytes : 0;
   static constexpr int kFit = (kGemmMaxSmem - 1024 - 512 - kOutBytes - kInBytes) / kStage;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kOut = kStages * kStage;
@@ -271,25 +283,28 @@ __device__ __forceinline__ void gemm_load(uint32_t dst, const CUtensorMap* map, 
   }
 }
 
-// Byte offset of 16-byte chunk `chunk` of row `row` of a 32 x 32 piece (rows of
-// 64 bytes, 64-byte swizzle).
-__device__ __forceinline__ uint32_t piece_offset(uint32_t row, uint32_t chunk) {
-  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
-}
-
-// An epilogue warp's staging ring: pieces leave by TMA stores, each waited for
+// An epilogue warp's staging: pieces leave by TMA stores, each waited for
 // (until read) before its place is written again.
+template <int COLS>
 struct PieceRing {
   uint8_t* base;
   int at;
-  __device__ __forceinline__ void store(const CUtensorMap* map, const uint32_t* w, int lane, int row, int col) {
-    uint8_t* p = base + at * kGemmPieceBytes;
-    at = at + 1 == kGemmOutPieces ? 0 : at + 1;
-    if (lane == 0) bulk_wait_read<kGemmOutPieces - 1>();
+  // f(i, w): 16 packed words of this lane's row, columns 32 i to 32 i + 31
+  template <typename F>
+  __device__ __forceinline__ void store(const CUtensorMap* map, int lane, int row, int col, const F& f) {
+    uint8_t* p = base + at * Piece<COLS>::kBytes;
+    at = at + 1 == Piece<COLS>::kSlots ? 0 : at + 1;
+    if (lane == 0) bulk_wait_read<Piece<COLS>::kSlots - 1>();
     __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4*>(p + piece_offset(lane, c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    for (int i = 0; i < COLS / 32; ++i) {
+      uint32_t w[16];
+      f(i, w);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(p + Piece<COLS>::offset(lane, 4 * i + c)) =
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -304,43 +319,48 @@ __device__ __forceinline__ void pack32(const uint32_t* r, uint32_t* w) {
   for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 
-// kEpiStore, kEpiGate: the outputs of one 32-row, 32-column piece from its
+// kEpiStore, kEpiGate: the outputs of one 32-row, 64-column piece from its
 // accumulator values r (kEpiGate: of g, and u of u).
 template <int EPI, int ACT>
 __device__ __forceinline__ void gemm_piece(const GemmArgs& P, const GemmProduct& Q, const uint32_t* r, const uint32_t* u,
-                                           PieceRing& ring, int lane, int row, int col) {
-  uint32_t w[16];
+                                           PieceRing<64>& ring, int lane, int row, int col) {
   if constexpr (EPI == kEpiStore) {
-    pack32(r, w);
-    ring.store(&Q.out[0], w, lane, row, col);
+    ring.store(&Q.out[0], lane, row, col, [&](int i, uint32_t* w) { pack32(r + 32 * i, w); });
   } else {
     // h from the fp32 projections, rounded once
+    ring.store(&Q.out[0], lane, row, col, [&](int i, uint32_t* w) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      w[i] = pack_bf16x2(act_f<ACT>(__uint_as_float(r[2 * i])) * __uint_as_float(u[2 * i]),
-                         act_f<ACT>(__uint_as_float(r[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
-    ring.store(&Q.out[0], w, lane, row, col);
+      for (int j = 0; j < 16; ++j) {
+        const int x = 32 * i + 2 * j;
+        w[j] = pack_bf16x2(act_f<ACT>(__uint_as_float(r[x])) * __uint_as_float(u[x]),
+                           act_f<ACT>(__uint_as_float(r[x + 1])) * __uint_as_float(u[x + 1]));
+      }
+    });
     if (P.save) {
-      pack32(r, w);
-      ring.store(&Q.out[1], w, lane, row, col);
-      pack32(u, w);
-      ring.store(&Q.out[2], w, lane, row, col);
+      ring.store(&Q.out[1], lane, row, col, [&](int i, uint32_t* w) { pack32(r + 32 * i, w); });
+      ring.store(&Q.out[2], lane, row, col, [&](int i, uint32_t* w) { pack32(u + 32 * i, w); });
     }
   }
 }
 
-// kEpiGateBwd: the outputs of one piece from dh in tensor memory at `acc` and
-// the saved projections' piece at `in` (gate, then up); `taken` once that is read.
+__device__ __forceinline__ void copy16(const uint32_t* from, uint32_t* to) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) to[i] = from[i];
+}
+
+// kEpiGateBwd: the outputs of one 32-row, 32-column piece from dh in tensor
+// memory at `acc` and the saved projections' piece at `in` (gate, then up);
+// `taken` once that is read.
 template <int ACT, typename F>
-__device__ __forceinline__ void gemm_piece_bwd(const GemmArgs& P, const GemmProduct& Q, uint32_t acc, PieceRing& ring,
+__device__ __forceinline__ void gemm_piece_bwd(const GemmArgs& P, const GemmProduct& Q, uint32_t acc, PieceRing<32>& ring,
                                                const uint8_t* in, int lane, int row, int col, const F& taken) {
   uint32_t r[32], w[16], wg[16], wu[16];
   tmem_ld32(acc, r);
   uint4 gv[4], uv[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    gv[c] = *reinterpret_cast<const uint4*>(in + piece_offset(lane, c));
-    uv[c] = *reinterpret_cast<const uint4*>(in + kGemmPieceBytes + piece_offset(lane, c));
+    gv[c] = *reinterpret_cast<const uint4*>(in + Piece<32>::offset(lane, c));
+    uv[c] = *reinterpret_cast<const uint4*>(in + Piece<32>::kBytes + Piece<32>::offset(lane, c));
   }
   __syncwarp();
   taken();
@@ -364,9 +384,9 @@ __device__ __forceinline__ void gemm_piece_bwd(const GemmArgs& P, const GemmProd
     wu[i] = pack_bf16x2(du[0], du[1]);
     w[i] = pack_bf16x2(h[0], h[1]);
   }
-  ring.store(&Q.out[0], wg, lane, row, col);
-  ring.store(&Q.out[1], wu, lane, row, col);
-  if (P.save) ring.store(&Q.out[2], w, lane, row, col);
+  ring.store(&Q.out[0], lane, row, col, [&](int, uint32_t* x) { copy16(wg, x); });
+  ring.store(&Q.out[1], lane, row, col, [&](int, uint32_t* x) { copy16(wu, x); });
+  if (P.save) ring.store(&Q.out[2], lane, row, col, [&](int, uint32_t* x) { copy16(w, x); });
 }
 
 template <int CG, int BN, int SUB, bool AMN, bool BMN, int EPI, int ACT>
@@ -522,12 +542,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;           // tensor memory lane quarter
     const int e = warp - 2;
-    const int c0 = (e >> 2) * kGemmPiece;  // of the two warps of a quarter, one takes the even pieces, one the odd
-    PieceRing ring = {sm + L::kOut + e * kGemmOutPieces * kGemmPieceBytes, 0};
-    uint8_t* in = sm + L::kIn + e * 2 * kGemmPieceBytes;  // gate, up
+    constexpr int kPiece = gemm_piece_cols(EPI);
+    const int c0 = (e >> 2) * kPiece;  // of the two warps of a quarter, one takes the even pieces, one the odd
+    PieceRing<kPiece> ring = {sm + L::kOut + e * kGemmOutBytes, 0};
+    uint8_t* in = sm + L::kIn + e * 2 * Piece<32>::kBytes;  // gate, up
     uint64_t* in_bar = in_full + e;
     constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;  // output columns of an accumulator
-    constexpr int kMine = kCols / (2 * kGemmPiece);       // pieces of this warp
+    constexpr int kMine = kCols / (2 * kPiece);           // pieces of this warp
     int j = 0, pieces = 0;
     bool ok = true;
     for (int u = cluster; u < P.units && ok; u += clusters) {
@@ -554,36 +575,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         if constexpr (EPI == kEpiGateBwd) {
           auto fetch = [&](int c) {  // the saved projections of the piece at column c
             if (c < end && lane == 0) {
-              mbar_arrive_expect_tx(in_bar, 2 * kGemmPieceBytes);
+              mbar_arrive_expect_tx(in_bar, 2 * Piece<32>::kBytes);
               tma_load_2d<1>(smem_u32(in), &P.in[0], smem_u32(in_bar), col + c, row);
-              tma_load_2d<1>(smem_u32(in) + kGemmPieceBytes, &P.in[1], smem_u32(in_bar), col + c, row);
+              tma_load_2d<1>(smem_u32(in) + Piece<32>::kBytes, &P.in[1], smem_u32(in_bar), col + c, row);
             }
           };
           fetch(c0);
           if (!wait_acc()) break;
 #pragma unroll 1
-          for (int c = c0; c < end; c += 2 * kGemmPiece, ++pieces) {
+          for (int c = c0; c < end; c += 2 * kPiece, ++pieces) {
             ok = __all_sync(0xffffffffu, mbar_wait_abortable(in_bar, pieces & 1, status, abort_flag));
             if (!ok) break;
             gemm_piece_bwd<ACT>(P, Q, t_acc + (c - c0), ring, in, lane, row, col + c,
-                                [&]() { fetch(c + 2 * kGemmPiece); });
+                                [&]() { fetch(c + 2 * kPiece); });
           }
           if (!ok) break;
           release_acc();
         } else {
           // all of this warp's values into registers, so that the accumulator is free at once
           if (!wait_acc()) break;
-          uint32_t r[kMine][32], v[EPI == kEpiGate ? kMine : 1][32];
+          uint32_t r[kMine][kPiece], v[EPI == kEpiGate ? kMine : 1][kPiece];
 #pragma unroll
-          for (int p = 0; p < kMine; ++p) {
-            tmem_ld32(t_acc + p * 2 * kGemmPiece, r[p]);
-            if constexpr (EPI == kEpiGate) tmem_ld32(t_acc + BN / 2 + p * 2 * kGemmPiece, v[p]);
-          }
+          for (int p = 0; p < kMine; ++p)
+#pragma unroll
+            for (int x = 0; x < kPiece; x += 32) {
+              tmem_ld32(t_acc + p * 2 * kPiece + x, r[p] + x);
+              if constexpr (EPI == kEpiGate) tmem_ld32(t_acc + BN / 2 + p * 2 * kPiece + x, v[p] + x);
+            }
           tmem_ld_wait();
           release_acc();
 #pragma unroll
           for (int p = 0; p < kMine; ++p) {
-            const int c = c0 + p * 2 * kGemmPiece;
+            const int c = c0 + p * 2 * kPiece;
             if (c < end) gemm_piece<EPI, ACT>(P, Q, r[p], v[EPI == kEpiGate ? p : 0], ring, lane, row, col + c);
           }
         }

@@ -33,12 +33,13 @@ inline prism_status gemm_operand_map(CUtensorMap* map, const GemmOperand& o, boo
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// A 32 x 32 piece of an [m, n] matrix, as the epilogue reads and writes it.
-inline prism_status gemm_piece_map(CUtensorMap* map, const void* base, int64_t m, int64_t n, int64_t ld) {
+// A piece of 32 rows of an [m, n] matrix, as the epilogue reads and writes it.
+inline prism_status gemm_piece_map(CUtensorMap* map, const void* base, int64_t m, int64_t n, int64_t ld, int cols) {
   const uint64_t dims[2] = {uint64_t(n), uint64_t(m)};
   const uint64_t strides[1] = {uint64_t(ld) * 2};
-  const uint32_t box[2] = {kGemmPiece, 32};
-  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+  const uint32_t box[2] = {uint32_t(cols), 32};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
+                      cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // The launch's attributes: the cluster, and for a product that follows another
@@ -81,12 +82,13 @@ prism_status gemm_launch(GemmArgs& P, const GemmProblem* pr, int products, cudaS
       if (R.b[g].base && st == PRISM_OK) st = gemm_operand_map(&Q.b[g], R.b[g], BMN, R.n, kb, kRowsB);
     }
     for (int g = 0; g < 3 && st == PRISM_OK; ++g)
-      if (R.out[g].base) st = gemm_piece_map(&Q.out[g], R.out[g].base, R.m, R.n, R.out[g].ld);
+      if (R.out[g].base) st = gemm_piece_map(&Q.out[g], R.out[g].base, R.m, R.n, R.out[g].ld, gemm_piece_cols(EPI));
     if (st != PRISM_OK) return st;
   }
   if constexpr (EPI == kEpiGateBwd) {
     prism_status st = PRISM_OK;
-    for (int g = 0; g < 2 && st == PRISM_OK; ++g) st = gemm_piece_map(&P.in[g], pr[0].in[g], pr[0].m, pr[0].n, pr[0].n);
+    for (int g = 0; g < 2 && st == PRISM_OK; ++g) st = gemm_piece_map(&P.in[g], pr[0].in[g], pr[0].m, pr[0].n, pr[0].n,
+                                                                      gemm_piece_cols(EPI));
     if (st != PRISM_OK) return st;
   }
   int clusters = device_sm_count() / CG;
