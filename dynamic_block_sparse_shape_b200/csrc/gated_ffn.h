@@ -13,7 +13,7 @@ prism_status ffn_gate_bwd_product(int act, GemmArgs& P, const GemmProblem& pr, c
 prism_status ffn_product_nt(GemmArgs& P, const GemmProblem& pr, cudaStream_t s);
 prism_status ffn_product_nn(GemmArgs& P, const GemmProblem& pr, cudaStream_t s);
 // the whole forward pass of at most kRowTokens tokens, y = x allowed; h: [m, f]
-constexpr int kRowTokens = 8;
+constexpr int kRowTokens = 32;
 prism_status ffn_rows_forward(int act, const prism_ffn_weights& w, int m, const void* x, int64_t x_ld, void* h, void* y,
                               int64_t y_ld, void* gate, void* up, cudaStream_t s);
 prism_status ffn_products_tn(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s);

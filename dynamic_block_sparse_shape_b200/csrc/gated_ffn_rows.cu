@@ -3,24 +3,26 @@
 // The mathematics: dot products of weight rows with every token,
 //   g_f = wg_f . x_m, u_f = wu_f . x_m, h_f = act(g_f) u_f,  then y_d = wd_d . h_m.
 //
-// What bounds it: the weights' bytes, read once (3 d f, at HBM's rate; a tile of
-// the tensor cores would be empty but for a few rows, and its 128-byte pieces
-// of 128 rows at a time reach 2 to 3 TB/s). So: fp32 multiply-adds on the
-// ordinary cores, weights in 16-byte loads, whole rows in order. A CTA takes R
-// weight rows; its warps take every eighth 256-value chunk of K, lane l the
-// values 8 l .. 8 l + 7, with the tokens' values in registers for all R rows and
-// the R loads of a chunk in flight together. Sums stay in fp32; lanes are
-// added by butterflies and warps in shared memory in a fixed order.
+// What bounds it: the weights' bytes, read once (3 d f, at HBM's rate). Tiles of
+// 128 rows by TMA fetch them in pieces of 128 bytes of 128 rows at a time, an SM
+// at most 90 GB/s; here every SM streams whole rows. A CTA takes 16 weight rows
+// (the gate product: 16 of Wg and the same 16 of Wu); its warps take blocks of K
+// in turn, with the next block's loads under way while one is multiplied. The products are warp-wide m16n8k16: a lane's 16 bytes of a row
+// are four pairs of k, and since the sum over k may go in any order, the pairs go
+// into the instruction as they lie: tokens are read with the same permutation,
+// and no value moves between lanes. Sums stay in fp32 and are added over the
+// warps in shared memory in a fixed order.
+// 2048 x 5632, cold weights: one token 18.2 us, 8 tokens 19.0, 16 23.2, 32 26.8 in
+// both launches (the tiles of the split kernel: 29 to 31; multiply-adds on the
+// ordinary cores: 18.8 for one token, 45 for 8).
 // The down product's first weights are requested before it waits for h
 // (programmatic dependent launch): they do not depend on it.
-// 2048 x 5632, one token: see the table in the design notes for both kernels' times.
 #include "gated_ffn.h"
 
 namespace prism {
 namespace {
 
-constexpr int kRowWarps = 8;
-constexpr int kRowChunk = 256;  // values of K per warp and step
+constexpr int kRowTile = 16;   // weight rows of a product
 
 struct RowArgs {
   const __nv_bfloat16* w[2];  // gate: Wg, Wu; down: Wd
@@ -33,79 +35,89 @@ struct RowArgs {
   int save;
 };
 
-// GATE: R / 2 rows of Wg, then the same of Wu; else R rows.
-template <int M, int R, bool GATE, int ACT>
-__global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowArgs P) {
-  constexpr int kOut = GATE ? R / 2 : R;  // output columns of a CTA
-  __shared__ float part[kRowWarps][R * M];
+__device__ __forceinline__ void mma_rows(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: groups of 8 tokens; U: steps of 32 values of K whose loads go together.
+// The gate product has twice the rows: few warps a CTA, several CTAs an SM.
+// The down product has few rows and a long K: many warps share them.
+constexpr int row_warps(bool gate) { return gate ? 4 : 16; }
+
+template <int NT, bool GATE, int ACT, int U>
+__global__ void __launch_bounds__(row_warps(GATE) * 32) rows_kernel(const RowArgs P) {
+  constexpr int kRowWarps = row_warps(GATE), kU = U, kRowBlock = 32 * U;
+  constexpr int kT = GATE ? 2 : 1;  // weight tiles
+  __shared__ float part[kRowWarps][kT * kRowTile][NT * 8 + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int f0 = blockIdx.x * kOut;
-  const __nv_bfloat16* row[R];
+  const int g = lane >> 2, t = lane & 3;  // of the instruction's fragments: row or token, and k pair
+  const int f0 = blockIdx.x * kRowTile;
+  const __nv_bfloat16* row[kT][2];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = GATE ? r / kOut : 0;
-    const int f = min(f0 + r % kOut, P.rows - 1);  // rows behind the last repeat it and are not written
-    row[r] = P.w[i] + f * P.w_ld[i];
-  }
-  float acc[R][M];
+  for (int i = 0; i < kT; ++i)
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+    for (int h = 0; h < 2; ++h)  // rows behind the last repeat it and are not written
+      row[i][h] = P.w[i] + min(f0 + g + 8 * h, P.rows - 1) * P.w_ld[i] + 8 * t;
+  const __nv_bfloat16* tok[NT];
 #pragma unroll
-    for (int m = 0; m < M; ++m) acc[r][m] = 0.f;
-  int k = warp * kRowChunk + lane * 8;
-  uint4 w[R];
+  for (int n = 0; n < NT; ++n) tok[n] = P.x + min(8 * n + g, P.m - 1) * P.x_ld + 8 * t;
+  float acc[kT][NT][4] = {};
+  uint4 w[kU][kT][2];
+  auto load = [&](int k, uint4 (&to)[kU][kT][2]) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) w[r] = k < P.k ? __ldg(reinterpret_cast<const uint4*>(row[r] + k)) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int i = 0; i < kT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          to[u][i][h] = k + 32 * u + 8 * t < P.k ? __ldg(reinterpret_cast<const uint4*>(row[i][h] + k + 32 * u))
+                                                 : make_uint4(0, 0, 0, 0);
+  };
+  int k = warp * kRowBlock;
+  load(k, w);
   grid_dependency_wait();
   grid_launch_dependents();
-  for (; k < P.k; k += kRowWarps * kRowChunk) {
-    // the next step's weights are on their way while this one is added
-    const int next = k + kRowWarps * kRowChunk;
-    uint4 wn[R];
+  for (; k < P.k; k += kRowWarps * kRowBlock) {
+    uint4 next[kU][kT][2];
+    load(k + kRowWarps * kRowBlock, next);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      wn[r] = next < P.k ? __ldg(reinterpret_cast<const uint4*>(row[r] + next)) : make_uint4(0, 0, 0, 0);
-    float x[M][8];
+    for (int u = 0; u < kU; ++u)
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const uint4 v = m < P.m ? *reinterpret_cast<const uint4*>(P.x + m * P.x_ld + k) : make_uint4(0, 0, 0, 0);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      for (int n = 0; n < NT; ++n) {
+        const uint4 x = k + 32 * u + 8 * t < P.k ? *reinterpret_cast<const uint4*>(tok[n] + k + 32 * u)
+                                                 : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[m][2 * i] = __uint_as_float(u[i] << 16);
-        x[m][2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        for (int i = 0; i < kT; ++i) {
+          mma_rows(acc[i][n], w[u][i][0].x, w[u][i][1].x, w[u][i][0].y, w[u][i][1].y, x.x, x.y);
+          mma_rows(acc[i][n], w[u][i][0].z, w[u][i][1].z, w[u][i][0].w, w[u][i][1].w, x.z, x.w);
+        }
       }
-    }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+    for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xFFFF0000u);
+      for (int i = 0; i < kT; ++i)
 #pragma unroll
-        for (int m = 0; m < M; ++m) acc[r][m] = fmaf(hi, x[m][2 * i + 1], fmaf(lo, x[m][2 * i], acc[r][m]));
-      }
-      w[r] = wn[r];
-    }
+        for (int h = 0; h < 2; ++h) w[u][i][h] = next[u][i][h];
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int i = 0; i < kT; ++i)
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      float s = acc[r][m];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) part[warp][r * M + m] = s;
-    }
+      for (int e = 0; e < 4; ++e) part[warp][i * kRowTile + g + 8 * (e >> 1)][8 * n + 2 * t + (e & 1)] = acc[i][n][e];
   __syncthreads();
-  for (int i = threadIdx.x; i < kOut * M; i += kRowWarps * 32) {
-    const int r = i / M, m = i - r * M, f = f0 + r;
+  for (int x = threadIdx.x; x < kRowTile * NT * 8; x += kRowWarps * 32) {
+    const int r = x % kRowTile, m = x / kRowTile, f = f0 + r;
     if (f >= P.rows || m >= P.m) continue;
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int v = 0; v < kRowWarps; ++v) {
-      a += part[v][r * M + m];
-      if constexpr (GATE) b += part[v][(r + kOut) * M + m];
+      a += part[v][r][m];
+      if constexpr (GATE) b += part[v][r + kRowTile][m];
     }
     if constexpr (GATE) {
       P.out[0][m * P.out_ld[0] + f] = __float2bfloat16_rn(act_f<ACT>(a) * b);
@@ -119,29 +131,37 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const RowArgs P) {
   }
 }
 
-template <int M, bool GATE, int ACT>
-prism_status launch_rows(const RowArgs& a, bool follows, cudaStream_t s) {
-  constexpr int R = M <= 4 ? 8 : 4;  // R M sums and 8 M values of x in registers
-  constexpr int kOut = GATE ? R / 2 : R;
+template <int NT, bool GATE, int ACT, int U>
+prism_status launch_rows_as(const RowArgs& a, bool follows, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((a.rows + kOut - 1) / kOut);
-  cfg.blockDim = dim3(kRowWarps * 32);
+  cfg.gridDim = dim3((a.rows + kRowTile - 1) / kRowTile);
+  cfg.blockDim = dim3(row_warps(GATE) * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = follows ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, rows_kernel<M, R, GATE, ACT>, a));
+  return cuda_status(cudaLaunchKernelEx(&cfg, rows_kernel<NT, GATE, ACT, U>, a));
+}
+
+// The down product of a small layer has a CTA per SM at most: 128 values at a
+// time keep more loads in flight (2048 x 5632, one token: 9.8 us, 13.0 with 64);
+// with more CTAs their registers count (4096 x 11264: 26.5 us, 22.7 with 64).
+template <int NT, bool GATE, int ACT>
+prism_status launch_rows(const RowArgs& a, bool follows, cudaStream_t s) {
+  if constexpr (!GATE) {
+    if ((a.rows + kRowTile - 1) / kRowTile <= device_sm_count()) return launch_rows_as<NT, GATE, ACT, 4>(a, follows, s);
+  }
+  return launch_rows_as<NT, GATE, ACT, 2>(a, follows, s);
 }
 
 template <bool GATE, int ACT>
 prism_status rows_for(const RowArgs& a, bool follows, cudaStream_t s) {
-  if (a.m == 1) return launch_rows<1, GATE, ACT>(a, follows, s);
-  if (a.m == 2) return launch_rows<2, GATE, ACT>(a, follows, s);
-  if (a.m <= 4) return launch_rows<4, GATE, ACT>(a, follows, s);
-  return launch_rows<8, GATE, ACT>(a, follows, s);
+  if (a.m <= 8) return launch_rows<1, GATE, ACT>(a, follows, s);
+  if (a.m <= 16) return launch_rows<2, GATE, ACT>(a, follows, s);
+  return launch_rows<4, GATE, ACT>(a, follows, s);
 }
 
 }  // namespace
