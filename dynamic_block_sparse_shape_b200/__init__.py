@@ -218,17 +218,25 @@ def workspace_size(op: str, geo: Geometry, heads=1, head_dim=128, feat_c=0, res_
 
 class Workspace:
     """A caller-owned device scratch buffer (torch allocation, 256-byte aligned)
-    that grows on demand. The library itself never allocates."""
+    that grows on demand. The library itself never allocates. A buffer that a
+    captured graph may hold stays allocated when a larger one takes its place."""
 
     def __init__(self, device="cuda", nbytes=1 << 20):
         self.device = torch.device(device)
         self.buf = None
+        self.captured = False  # `buf` was used under a stream capture
+        self.kept = []
         self.ensure(nbytes)
 
     def ensure(self, nbytes: int):
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.captured:
+                self.kept.append(self.buf)
             self.buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
+            self.captured = False
+        if self.buf.is_cuda and torch.cuda.is_current_stream_capturing():
+            self.captured = True
         return self
 
     @property

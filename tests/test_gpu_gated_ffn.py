@@ -112,3 +112,220 @@ def test_large_tiles(m, d, f):
     P.check_device_status(ws)
     check_fwd(x, wg, wu, wd, "silu", y, g, u)
     check_bwd(dy, x, wg, wu, wd, g, u, "silu", got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 20, 100, 300, 2100])
+def test_views_and_what_lies_around(m):
+    """Weights as the halves of one matrix, padded rows everywhere; nothing outside the outputs changes."""
+    require_gpu()
+    d, f = 264, 136 if m < 2000 else 2056
+    x, wg, wu, wd, dy = draw(m, d, f, m)
+    both = torch.full((2 * f, d + 24), 9.0, dtype=torch.bfloat16, device="cuda")
+    both[:f, :d], both[f:, :d] = wg, wu
+    wdp = torch.full((d, f + 8), 9.0, dtype=torch.bfloat16, device="cuda")
+    wdp[:, :f] = wd
+    buf = torch.full((m + 3, d + 40), -7.0, dtype=torch.bfloat16, device="cuda")
+    xp, yp = buf.clone(), buf.clone()
+    xp[:m, :d] = x
+    ws = P.Workspace("cuda")
+    y, g, u = P.gated_ffn_fwd(x, wg, wu, wd, ws=ws)
+    got, g2, u2 = P.gated_ffn_fwd(xp[:m, :d], both[:f, :d], both[f:, :d], wdp[:, :f], out=yp[:m, :d], ws=ws)
+    assert got.data_ptr() == yp.data_ptr() and torch.equal(got, y) and torch.equal(g, g2) and torch.equal(u, u2)
+    assert (yp[m:] == -7).all() and (yp[:, d:] == -7).all()
+    P.gated_ffn_fwd(xp[:m, :d], both[:f, :d], both[f:, :d], wdp[:, :f], out=xp[:m, :d], save=False, ws=ws)  # y over x
+    assert torch.equal(xp[:m, :d], y) and (xp[m:] == -7).all() and (xp[:, d:] == -7).all()
+    dyp = buf.clone()
+    dyp[:m, :d] = dy
+    xp[:m, :d] = x
+    a = P.gated_ffn_bwd(dy, x, wg, wu, wd, g, u, ws=ws)
+    b = P.gated_ffn_bwd(dyp[:m, :d], xp[:m, :d], both[:f, :d], both[f:, :d], wdp[:, :f], g, u, ws=ws)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    P.check_device_status(ws)
+
+
+def _outputs_in(buffers):
+    """Views of the middle of canary-filled buffers."""
+    return [b[64:64 + n].view(shape) for b, n, shape in buffers]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [1, 9, 33, 129, 2305])
+def test_backward_writes_only_its_outputs(m):
+    require_gpu()
+    d, f = 328, 1288
+    x, wg, wu, wd, dy = draw(m, d, f, 3)
+    ws = P.Workspace("cuda")
+    _, g, u = P.gated_ffn_fwd(x, wg, wu, wd, ws=ws)
+    want = P.gated_ffn_bwd(dy, x, wg, wu, wd, g, u, ws=ws)
+    shapes = [(m, d), (f, d), (f, d), (d, f)]
+    bufs = [(torch.full((a * b + 128,), 5.0, dtype=torch.bfloat16, device="cuda"), a * b, (a, b)) for a, b in shapes]
+    dx, dwg, dwu, dwd = _outputs_in(bufs)
+    w, _, _ = P._ffn_weights(wg, wu, wd, "test")
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    st = P.lib().prism_gated_ffn_bwd(ctypes.byref(w), m, 0, 0, p(dy), d, p(x), d, p(g), p(u), p(dx), d, p(dwg), p(dwu),
+                                     p(dwd), ws.ptr, ws.nbytes, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    for t, r, (b, n, _) in zip((dx, dwg, dwu, dwd), want, bufs):
+        assert torch.equal(t, r) and (b[:64] == 5).all() and (b[64 + n:] == 5).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [3, 40, 700])
+def test_rows_are_apart(m):
+    """NaN and infinities of one token stay in its row, whatever tile it shares."""
+    require_gpu()
+    d, f = 1160, 1032
+    x, wg, wu, wd, dy = draw(m, d, f, 4)
+    y, g, u = P.gated_ffn_fwd(x, wg, wu, wd)
+    bad = m // 2
+    x2, dy2 = x.clone(), dy.clone()
+    x2[bad] = float("nan")
+    y2, g2, u2 = P.gated_ffn_fwd(x2, wg, wu, wd)
+    keep = torch.arange(m, device="cuda") != bad
+    assert torch.isnan(y2[bad]).all() and torch.equal(y2[keep], y[keep])
+    dy2[bad] = float("inf")
+    a = P.gated_ffn_bwd(dy, x, wg, wu, wd, g, u, need_dw=False)[0]
+    b = P.gated_ffn_bwd(dy2, x, wg, wu, wd, g, u, need_dw=False)[0]
+    assert not torch.isfinite(b[bad]).any() and torch.equal(b[keep], a[keep])
+
+
+@pytest.mark.gpu
+def test_empty_streams_and_graphs():
+    require_gpu()
+    d, f = 256, 512
+    x, wg, wu, wd, dy = draw(300, d, f, 6)
+    y, g, u = P.gated_ffn_fwd(x[:0], wg, wu, wd)
+    assert y.shape == (0, d) and g.shape == (0, f)
+    dx, dwg, dwu, dwd = P.gated_ffn_bwd(dy[:0], x[:0], wg, wu, wd, g, u)
+    assert dx.shape == (0, d) and all((t == 0).all() for t in (dwg, dwu, dwd))
+    want = P.gated_ffn_fwd(x, wg, wu, wd)
+    wantb = P.gated_ffn_bwd(dy, x, wg, wu, wd, want[1], want[2])
+    # another stream, with no workspace given: its memory is not handed on before the stream is done with it
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [P.gated_ffn_fwd(x, wg, wu, wd, stream=side) for _ in range(8)]
+    junk = [torch.full((300, f), 3.0, device="cuda") for _ in range(8)]
+    side.synchronize()
+    assert all(torch.equal(a, b) for r in got for a, b in zip(r, want)) and len(junk) == 8
+    # two captured graphs that share a workspace, replayed in turn on one stream, after eager calls that grow it
+    ws = P.Workspace("cuda")
+    graphs = []
+    for m in (7, 300):
+        xs = x[:m].clone()
+        P.gated_ffn_fwd(xs, wg, wu, wd, ws=ws)
+        P.gated_ffn_bwd(dy[:m], xs, wg, wu, wd, want[1][:m].clone(), want[2][:m].clone(), ws=ws)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            yy, gg, uu = P.gated_ffn_fwd(xs, wg, wu, wd, ws=ws)
+            bb = P.gated_ffn_bwd(dy[:m], xs, wg, wu, wd, gg, uu, ws=ws)
+        graphs.append((gr, m, yy, bb))
+    held = ws.buf.numel()
+    ws.ensure(1 << 26)  # a larger buffer: the graphs' own stays theirs
+    junk = [torch.full((held,), 3, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for _ in range(2):
+        for gr, m, yy, bb in graphs:
+            gr.replay()
+    torch.cuda.synchronize()
+    assert all((j == 3).all() for j in junk)
+    for gr, m, yy, bb in graphs:
+        r = P.gated_ffn_fwd(x[:m], wg, wu, wd)
+        rb = P.gated_ffn_bwd(dy[:m], x[:m], wg, wu, wd, r[1], r[2])
+        assert torch.equal(yy, r[0]) and all(torch.equal(a, b) for a, b in zip(bb, rb))
+    assert all(torch.equal(a, b) for a, b in zip(wantb, graphs[1][3]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,stride", [(20, 1 << 28), (300, 1 << 24)])
+def test_offsets_past_32_bits(m, stride):
+    """Tokens more than 2^32 elements apart (10 GB between the first and the last)."""
+    require_gpu()
+    d, f = 136, 264
+    x, wg, wu, wd, dy = draw(m, d, f, 8)
+    want = P.gated_ffn_fwd(x, wg, wu, wd)
+    wantb = P.gated_ffn_bwd(dy, x, wg, wu, wd, want[1], want[2])
+    buf = torch.empty((m - 1) * stride + d, dtype=torch.bfloat16, device="cuda")
+    far = buf.as_strided((m, d), (stride, 1))
+    far.copy_(x)
+    got = P.gated_ffn_fwd(far, wg, wu, wd)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    gotb = P.gated_ffn_bwd(dy, far, wg, wu, wd, want[1], want[2])
+    assert all(torch.equal(a, b) for a, b in zip(gotb, wantb))
+    P.gated_ffn_fwd(x, wg, wu, wd, out=far)
+    assert torch.equal(far, want[0])
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_formulas_against_differences(act):
+    """The fp64 gradient formulas that the kernels are held to, against central differences of the fp64 forward."""
+    r = np.random.default_rng(1)
+    m, d, f = 3, 5, 7
+    x, wg, wu, wd, dy = r.normal(size=(m, d)), r.normal(size=(f, d)), r.normal(size=(f, d)), r.normal(size=(d, f)), \
+        r.normal(size=(m, d))
+    _, g, u = O.gated_ffn_fwd(x, wg, wu, wd, act)
+    grads = O.gated_ffn_bwd(dy, x, wg, wu, wd, g, u, act)
+    loss = lambda *a: float((O.gated_ffn_fwd(*a, act)[0] * dy).sum())  # noqa: E731
+    args, h = [x, wg, wu, wd], 1e-6
+    for i, grad in enumerate(grads):
+        for _ in range(6):
+            v = r.normal(size=args[i].shape)
+            up, down = [list(args) for _ in range(2)]
+            up[i], down[i] = args[i] + h * v, args[i] - h * v
+            # truncation h^2 times a third derivative of order 10, rounding 1e-15 / h times the loss of order 100
+            assert abs((loss(*up) - loss(*down)) / (2 * h) - float((grad * v).sum())) < 1e-6
+
+
+def _weights(**change):
+    w = P._FfnWeights(1 << 20, 1 << 22, 1 << 24, 64, 64, 128, 64, 128)
+    for k, v in change.items():
+        setattr(w, k, v)
+    return w
+
+
+def test_refusals():
+    """Every refused call returns its status before any CUDA call."""
+    from dynamic_block_sparse_shape_b200 import build
+    build.build()
+    lib, big = P.lib(), 1 << 40
+    A = 1 << 30  # activations' addresses from here on, far from the weights
+
+    def fwd(w=None, m=4, act=0, dtype=0, x=A, sx=64, y=A + (1 << 16), sy=64, gate=None, up=None, ws=1 << 34, nb=big):
+        return lib.prism_gated_ffn_fwd(ctypes.byref(w or _weights()), m, act, dtype, x, sx, y, sy, gate, up, ws, nb, None)
+
+    def bwd(w=None, m=4, act=0, dtype=0, dy=A, sdy=64, x=A + (1 << 16), sx=64, gate=A + (2 << 16), up=A + (3 << 16),
+            dx=A + (4 << 16), sdx=64, g=A + (5 << 16), u=A + (6 << 16), d=A + (7 << 16), ws=1 << 34, nb=big):
+        return lib.prism_gated_ffn_bwd(ctypes.byref(w or _weights()), m, act, dtype, dy, sdy, x, sx, gate, up, dx, sdx, g,
+                                       u, d, ws, nb, None)
+
+    for call in (fwd, bwd):
+        assert call(dtype=1) == 3 and call(act=4) == 1 and call(act=-1) == 1 and call(m=-1) == 1
+        assert call(m=(1 << 30) + 1) == 9
+        assert call(_weights(d=60, gate_stride=64, up_stride=64)) == 9 and call(_weights(f=132)) == 9
+        assert call(_weights(w_gate=None)) == 1 and call(_weights(w_up=(1 << 22) + 8)) == 1
+        assert call(_weights(gate_stride=56)) == 1 and call(_weights(down_stride=130)) == 1
+        assert call(_weights(up_stride=1 << 31)) == 9
+        assert call(x=None) == 1 and call(x=A + (1 << 16) + 8) == 1 and call(sx=60) == 1
+        assert call(ws=None) == 4 and call(ws=(1 << 34) + 8) == 4 and call(nb=256) == 4
+    assert fwd(y=None) == 1 and fwd(sy=72 + 4) == 1
+    assert fwd(gate=A + (2 << 16)) == 1 and fwd(gate=A + (2 << 16), up=A + (2 << 16) + 8) == 1
+    assert fwd(gate=A + (2 << 16), up=A + (2 << 16) + 256) == 1  # the projections over one another
+    assert fwd(gate=A, up=A + (2 << 16)) == 1 and fwd(gate=1 << 24, up=A + (2 << 16)) == 1  # over x, over a weight
+    assert fwd(y=1 << 24) == 1  # y over the second weight
+    assert bwd(dx=None, g=None, u=None, d=None) == 1 and bwd(u=None) == 1
+    assert bwd(dy=None) == 1 and bwd(gate=None) == 1 and bwd(up=A + 8) == 1 and bwd(sdx=65) == 1
+    assert bwd(dx=A) == 1 and bwd(dx=A + (1 << 16) + 128) == 1  # over dy, over part of x
+    assert bwd(g=A + (6 << 16)) == 1 and bwd(d=1 << 20) == 1  # outputs over one another, over a weight
+    b = ctypes.c_size_t()
+    assert lib.prism_gated_ffn_workspace_size(-1, 8, 0, ctypes.byref(b)) == 1
+    assert lib.prism_gated_ffn_workspace_size(4, 8, 0, None) == 1
+    assert lib.prism_gated_ffn_workspace_size(1 << 31, 8, 0, ctypes.byref(b)) == 9
+    assert lib.prism_gated_ffn_workspace_size(1000, 128, 1, ctypes.byref(b)) == 0 and b.value == 256 + 3 * 256000
+    x, wg, wu, wd, dy = draw(4, 64, 128, 1, device="cpu")
+    for bad in (dict(act="tanh"), dict()):  # an activation that is none; not on a GPU
+        with pytest.raises(P.PrismError):
+            P.gated_ffn_fwd(x, wg, wu, wd, **bad)
+    for args in ((x, wg[:64], wu, wd), (x, wg, wu.t(), wd), (x[:, :32], wg, wu, wd), (x.float(), wg, wu, wd),
+                 (x, wg, wu, wd[:, ::2])):
+        with pytest.raises(P.PrismError):
+            P.gated_ffn_fwd(*args)
