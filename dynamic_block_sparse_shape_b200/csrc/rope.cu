@@ -29,6 +29,11 @@
 // The half layout with a half that is no multiple of 16 bytes goes through
 // rope_staged_kernel: whole rows in 16-byte vectors to shared memory, rotated
 // there in place by narrower vectors, and back in 16-byte vectors.
+//
+// With one or two heads the angles are most of the work and the kernel is bound
+// by instructions (2.6 times the floor for one head each of Q and K, 101 pairs);
+// the hardware's approximate sine and cosine would take 8 % off that and lose
+// three bits, so the exact ones stay.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -116,6 +121,12 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src) {
 
 // m cos a and m sin a (signed) of the CTA's tokens n0 .. n0 + end - 1, all pairs.
 __device__ __forceinline__ void rope_angles(const RopeArgs& P, int64_t n0, int end, float* cosines, float* sines) {
+  // Every lane wants another pair's entry: constant memory would serve one lane
+  // at a time, so the tables are read as ordinary memory (the compiler cannot
+  // see through the address any more).
+  const uint64_t* turn = P.turn;
+  const uint64_t* start = P.start;
+  asm("" : "+l"(turn), "+l"(start));
   for (int x = threadIdx.x; x < end * P.pairs; x += blockDim.x) {
     const int tok = quotient(x, P.by_pairs), i = x - tok * P.pairs;
     const int64_t n = n0 + tok;
@@ -127,7 +138,7 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& P, int64_t n0, int e
       const uint32_t row = quotient(uint32_t(n), P.by_w), t = quotient(row, P.by_h);
       p = axis == 2 ? int(uint32_t(n) - row * P.by_w.d) : axis == 1 ? int(row - t * P.by_h.d) : int(t);
     }
-    const uint64_t turns = uint64_t(int64_t(p)) * P.turn[i] + P.start[i];
+    const uint64_t turns = uint64_t(int64_t(p)) * turn[i] + start[i];
     float s, c;
     sincospif(float(int32_t(turns >> 32)) * (1.f / 2147483648.f), &s, &c);
     cosines[x] = c * P.m;
@@ -503,13 +514,9 @@ extern "C" prism_status prism_rope(const prism_rope_params* params, const prism_
   // a CTA: `units` threads per head, the heads of Q and of K in equal steps, then tokens side by side
   const int fit = kRopeThreads / a.units < kRopeMaxHeadGroups ? kRopeThreads / a.units : kRopeMaxHeadGroups;
   a.head_groups = 1;
-  int best = 1 << 30;
-  for (int g = 1; g <= fit; ++g) {  // the fewest idle places, then the fewest steps
-    const int idle = (g - heads_q % g) % g + (hk ? (g - hk % g) % g : 0);
-    if (idle <= best) {
-      best = idle;
-      a.head_groups = g;
-    }
+  for (int g = 2; g <= fit; ++g) {  // the most heads side by side that leave at most a tenth of the places idle
+    const int64_t places = (int64_t(heads_q + g - 1) / g + (hk + g - 1) / g) * g;
+    if (places * 10 <= int64_t(heads_q + hk) * 11) a.head_groups = g;
   }
   a.token_groups = kRopeThreads / (a.units * a.head_groups);
   // tokens of a CTA: its vectors fill kRopeSmem; few tokens: fewer, for as many SMs as possible
