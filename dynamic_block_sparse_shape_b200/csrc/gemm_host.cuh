@@ -114,6 +114,15 @@ prism_status gemm_launch(GemmArgs& P, const GemmProblem* pr, int products, cudaS
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, P));
 }
 
+// CTAs that run at once in clusters of `ranks`, one or two per SM: a cluster
+// stays within a group of SMs, and what is left over of the groups stays idle
+// (as the occupancy query says for a B200: 148, 148, 132, 120 CTAs in clusters of
+// 1, 2, 4, 8 at one per SM, 296, 296, 284, 264 at two).
+inline int64_t split_slots(int ranks, int per_sm) {
+  const int idle = ranks >= 8 ? (per_sm == 1 ? 28 : 32) : ranks >= 4 ? (per_sm == 1 ? 16 : 12) : 0;
+  return int64_t(device_sm_count()) * per_sm - idle;
+}
+
 template <int CG, int BN, bool AMN, bool BMN, int EPI, int ACT>
 prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int products, int parts, cudaStream_t s) {
   constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;
@@ -153,7 +162,7 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
   const int ranks = CG * parts;
   if (tiles * ranks >= (int64_t(1) << 31)) return PRISM_ERR_UNSUPPORTED;
   // a ring of all of an SM's shared memory, or two of half of it
-  const int room = CG == 2 || (tiles * ranks <= device_sm_count() && ranks < kSplitMax) ? kGemmMaxSmem : 113 * 1024;
+  const int room = CG == 2 || tiles * ranks <= split_slots(ranks, 1) ? kGemmMaxSmem : 113 * 1024;
   A.stages = int(std::min<int64_t>(kSplitStages, (slices + parts - 1) / parts));
   while (A.stages > 1 && split_smem(CG, BN, A.a_bytes, A.stages) > room) --A.stages;
   const int smem = split_smem(CG, BN, A.a_bytes, A.stages);
@@ -212,14 +221,20 @@ inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, 
     const int rows_a = a_mn || t.cg == 2 || m[0] >= kGemmM ? kGemmM : int(m[0] + 7) / 8 * 8;
     const double bytes = (rows_a + t.bn / t.cg) * 128.0;
     for (int parts = 1; parts <= t.parts && parts <= slices; parts *= 2) {
-      const double ctas = tiles(kGemmM * t.cg, t.bn) * t.cg * parts, per_sm = std::ceil(ctas / sms);
+      const int64_t ctas = int64_t(tiles(kGemmM * t.cg, t.bn)) * t.cg * parts, one_each = split_slots(t.cg * parts, 1);
+      // rounds of CTAs, and how many an SM works through in all
+      int64_t rounds = (ctas + one_each - 1) / one_each, load = rounds;
+      if (t.cg == 1 && rounds > 1) {
+        const int64_t two_each = split_slots(parts, 2);
+        rounds = (ctas + two_each - 1) / two_each;
+        load = 2 * rounds - (ctas - (rounds - 1) * two_each <= one_each);
+      }
       const double mine = std::ceil(k / parts);
-      const double flight = std::fmin(std::fmin(mine, double(kSplitStages)) * (t.cg == 2 ? 1.0 : std::fmin(per_sm, 2.0)),
+      const double flight = std::fmin(std::fmin(mine, double(kSplitStages)) * (t.cg == 1 && load > 1 ? 2.0 : 1.0),
                                       kGemmMaxSmem / bytes);
       const double slice = std::fmax(std::fmax(bytes / rate, kSliceNs), kLatencyNs / std::fmax(flight, 1.0));
-      const double rounds = t.cg == 2 ? per_sm : std::ceil(per_sm / 2);
-      const double join = parts > 1 ? rounds * kJoinNs + per_sm * rows_a * t.bn * 4.0 / kJoinRate : 0.0;
-      const double ns = per_sm * mine * slice + rounds * kTileNs + join;
+      const double join = parts > 1 ? double(rounds) * kJoinNs + double(load) * rows_a * t.bn * 4.0 / kJoinRate : 0.0;
+      const double ns = double(load) * mine * slice + double(rounds) * kTileNs + join;
       if (ns < best) {
         best = ns;
         c = {t.cg, t.bn, parts};
