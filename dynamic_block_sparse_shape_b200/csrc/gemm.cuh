@@ -115,11 +115,38 @@ __device__ __forceinline__ float sigmoid_f(float z) {
   return s;
 }
 
+// Phi(g) and exp(-g^2 / 2). With x = |g| / sqrt(2), erfc(x) = exp(-x^2) erfcx(x), and
+// erfcx is smooth: a polynomial of degree 9 in t = 1 / (1 + x / 2), fitted to it
+// over [0, 10.5] by reweighted least squares (relative error 4e-8, 3.3e-7 in fp32
+// arithmetic). It keeps its relative precision where Phi is small, and the
+// derivative shares its exponential; the library's erfc took three times as many
+// instructions, which thin products (few values of K per output) waited for.
+__device__ __forceinline__ void normal_f(float g, float& cdf, float& e) {
+  const float x = fabsf(g) * 0.70710678118654752f;
+  float t;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.5f, x, 1.f)));
+  float p = -0.0591926179f;
+  p = fmaf(p, t, 0.285179633f);
+  p = fmaf(p, t, -0.488454836f);
+  p = fmaf(p, t, 0.279506303f);
+  p = fmaf(p, t, -0.0276195063f);
+  p = fmaf(p, t, 0.203108422f);
+  p = fmaf(p, t, 0.242996956f);
+  p = fmaf(p, t, 0.282390025f);
+  p = fmaf(p, t, 0.282085577f);
+  const float q = 0.5f * e * (p * t);
+  cdf = g < 0.f ? q : 1.f - q;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_f(float g) {
   if constexpr (ACT == PRISM_ACT_SILU) return g * sigmoid_f(g);
-  // g Phi(g) through erfc, which has no cancellation where Phi is small
-  if constexpr (ACT == PRISM_ACT_GELU) return 0.5f * g * erfcf(-0.70710678118654752f * g);
+  if constexpr (ACT == PRISM_ACT_GELU) {
+    float p, e;
+    normal_f(g, p, e);
+    return g * p;
+  }
   // (1 + tanh z) / 2 = sigmoid(2 z)
   if constexpr (ACT == PRISM_ACT_GELU_TANH)
     return g * sigmoid_f(1.5957691216057308f * (g + 0.044715f * g * g * g));
@@ -134,9 +161,10 @@ __device__ __forceinline__ void act_slope_f(float g, float& a, float& slope) {
     a = g * s;
     slope = s + a * (1.f - s);
   } else if constexpr (ACT == PRISM_ACT_GELU) {
-    const float p = 0.5f * erfcf(-0.70710678118654752f * g);
+    float p, e;
+    normal_f(g, p, e);
     a = g * p;
-    slope = p + g * 0.39894228040143268f * __expf(-0.5f * g * g);
+    slope = fmaf(g * 0.39894228040143268f, e, p);
   } else if constexpr (ACT == PRISM_ACT_GELU_TANH) {
     const float s = sigmoid_f(1.5957691216057308f * (g + 0.044715f * g * g * g));
     a = g * s;
