@@ -489,6 +489,77 @@ def measure_selection_variants(pipe, res, peaks, peak_src, reps=5):
     return out
 
 
+FFN_WIDTH = 8192  # inner width of the feed-forward block timed behind the layer
+
+
+def measure_around_attention(pipe, peaks, peak_src, reps=3):
+    """Per-call times of the operators around the layer's attention, outside the timed step (CUDA events, same
+    stream): the rotation of Q and K over the grid and of dQ and dK back, a gated feed-forward block (inner width
+    FFN_WIDTH, random weights) on the attention's output with its backward pass, and the clipping of all six
+    gradients. HBM streams against the copy bandwidth (algorithmic bytes), the block against the sustained bf16 rate."""
+    import torch
+    P, wl, x = pipe.P, pipe.wl, pipe.x
+    n, H, d = x["q"].shape
+    dev, hbm, tensor = x["q"].device, float(peaks.get("hbm_gbs")), float(
+        peaks.get("bf16_tflops_sustained", peaks.get("bf16_tflops")))
+
+    def timed(fn):
+        fn()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(reps):
+            fn()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / reps
+
+    def stream(ms, nbytes):
+        gbs = nbytes / (ms * 1e-3) / 1e9
+        return {"ms": round(ms, 4), "bound": "hbm", "achieved": round(gbs, 1), "peak": hbm, "unit": "GB/s",
+                "frac": round(gbs / hbm, 4), "algorithmic_bytes": nbytes, "peak_source": f"{peak_src} copy bandwidth"}
+
+    def product(ms, flop):
+        tf = flop / (ms * 1e-3) / 1e12
+        return {"ms": round(ms, 4), "bound": "tensor", "achieved": round(tf, 1), "peak": tensor, "unit": "TFLOP/s",
+                "frac": round(tf / tensor, 4), "peak_source": f"{peak_src} bf16 sustained"}
+
+    out = {}
+    side = d // 6 * 2
+    spec = P.RopeSpec((d - 2 * side, side, side))
+    turned = (torch.empty_like(x["q"]), torch.empty_like(x["k"]))
+    nbytes = 4 * x["q"].numel() * x["q"].element_size()
+    out["rope"] = stream(timed(lambda: P.rope(x["q"], x["k"], spec, grid=wl.grid, out=turned)), nbytes)
+    if not pipe.backward:
+        return out
+    dq, dk, dv = pipe.grads
+    out["rope_bwd"] = stream(timed(lambda: P.rope_bwd(dq, dk, spec, grid=wl.grid, out=turned)), nbytes)
+    c, f = H * d, FFN_WIDTH
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(1)
+    weight = lambda rows, cols: (torch.randn((rows, cols), generator=gen, device=dev) * cols ** -0.5).to(torch.bfloat16)  # noqa: E731
+    weights = (weight(f, c), weight(f, c), weight(c, f))
+    h, dy = pipe.o.view(n, c), x["do"].view(n, c)
+    state = {}
+
+    def fwd():
+        state["saved"] = P.gated_ffn_fwd(h, *weights, act="gelu_tanh", ws=pipe.ws)[1:]
+
+    def bwd():
+        state["grads"] = P.gated_ffn_bwd(dy, h, *weights, *state["saved"], act="gelu_tanh", ws=pipe.ws)
+
+    out["gated_ffn_fwd"] = product(timed(fwd), 6.0 * n * c * f)
+    out["gated_ffn_bwd"] = product(timed(bwd), 12.0 * n * c * f)
+    # into other tensors, so that every call finds the unclipped gradients
+    both = [dq, dk, dv, *state["grads"][1:]]
+    grads = P.GradList(both, out=[torch.empty_like(t) for t in both])
+    moved = sum(t.numel() * t.element_size() for t in both)
+    # read for the norm, read and written for the scaling
+    out["clip_grad_norm"] = stream(timed(lambda: P.clip_grad_norm(grads, 1.0, ws=pipe.ws)), 3 * moved)
+    P.check_device_status(pipe.ws)
+    return out
+
+
 def run_gpu(args):
     import torch
     import torch.distributed as dist
@@ -541,6 +612,7 @@ def run_gpu(args):
     e2e = None if args.no_e2e else run_e2e(pipe, wl, x, feats, res, steps=min(args.steps, args.e2e_steps))
     peaks, peak_src = _peaks()
     variants = measure_selection_variants(pipe, res, peaks, peak_src)
+    around = measure_around_attention(pipe, peaks, peak_src) if world == 1 else None
     nnz = pipe.nnz
     flop_per_pair = FWD_FLOP_PER_PAIR + (BWD_FLOP_PER_PAIR if pipe.backward else 0)
     attn_flop = nnz * flop_per_pair
@@ -571,6 +643,7 @@ def run_gpu(args):
                      "flop_per_pair": flop_per_pair},
         "roofline_selection_path": selection_path_roofline(wl, stage_ms, feats, res, peaks, peak_src, pipe.nb),
         "selection_variants": variants,
+        "around_attention": around,
         "e2e": e2e,
         "gpu_launches": pipe.launches_per_step() * args.steps,
         "clocks": clocks,

@@ -715,11 +715,23 @@ def gated_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up:
 _NORM = {2: 0, 2.0: 0, "l2": 0, math.inf: 1, "inf": 1}
 
 
+def _dense(t: torch.Tensor) -> bool:
+    """Whether the values fill one run of memory, in any order of the dimensions."""
+    if t.is_contiguous():
+        return True
+    run = 1
+    for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != run:
+            return False
+        run *= size
+    return True
+
+
 class GradList:
     """A list of gradients (and where their scaled values go) for ``grad_norm``, ``scale_grads`` and
     ``clip_grad_norm``, laid out once: a program whose gradients stay in place keeps it from step to step. It holds
-    the tensors, so their memory stays theirs. grads: dense contiguous bf16 / fp32 tensors of one device, any mix; out:
-    None (in place) or one tensor for each, of its size and type."""
+    the tensors, so their memory stays theirs. grads: dense bf16 / fp32 tensors of one device, any mix, in any order of
+    their dimensions; out: None (in place) or one tensor for each, of its shape, strides and type."""
 
     def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None):
         self.grads = list(grads)
@@ -729,13 +741,14 @@ class GradList:
         self.device = self.grads[0].device if n else None
         self._c = (_Tensor * max(n, 1))()
         for i, t in enumerate(self.grads):
-            _require(t.is_contiguous(), "GradList: gradients must be contiguous")
+            _require(_dense(t), "GradList: gradients must be dense")
             _require(t.device == self.device, "GradList: gradients on different devices")
             o = None
             if self.out is not None:
                 o = self.out[i]
-                _require(o.is_contiguous() and o.numel() == t.numel() and o.dtype == t.dtype and
-                         o.device == self.device, "GradList: an output is not like its gradient")
+                _require(o.shape == t.shape and o.dtype == t.dtype and o.device == self.device and
+                         (o.stride() == t.stride() or (o.is_contiguous() and t.is_contiguous())),
+                         "GradList: an output is not like its gradient")
                 o = o.data_ptr()
             self._c[i] = (t.data_ptr(), o, t.numel(), _dtype_code(t), 0)
         b = _SZ()

@@ -133,7 +133,7 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
     if ((st = check_rows(r)) != PRISM_OK) return st;
   const bool dw = dw_gate || dw_up || dw_down;
   if (dw && !(dw_gate && dw_up && dw_down)) return PRISM_ERR_ARG;
-  if (!dx && !dw) return PRISM_ERR_ARG;
+  if (m > 0 && !dx && !dw) return PRISM_ERR_ARG;
   for (const void* p : {dw_gate, dw_up, dw_down})
     if (reinterpret_cast<uintptr_t>(p) % 16) return PRISM_ERR_ARG;
   if (m > 0) {

@@ -132,6 +132,7 @@ struct Chunk {
     }
     const float s = s0 + s1;
     if (!tiny_or_over(s)) return double(s);
+    if (s == 0.f && max_bits() == 0) return 0.0;  // gradients that are all zero, not just small
     double d = 0.0;
 #pragma unroll
     for (int i = 0; i < kGnVecs; ++i) {
@@ -292,7 +293,8 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) scale_kernel(const _
   const double norm = S.partial ? combine(S.partial, S.parts, S.inf_norm) : double(*S.norm);
   if (S.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *S.norm = float(norm);
   const double f = double(S.max_norm) / (norm + double(S.eps));
-  const float factor = f >= 1.0 ? 1.f : float(f);  // a NaN norm makes every value NaN
+  // a NaN norm makes every value NaN, unless there is nothing to clip to
+  const float factor = f >= 1.0 || isinf(S.max_norm) ? 1.f : float(f);
   auto skip = [&](int c) {  // nothing to do for chunk c; also finds its item
     if (T.item[it].chunk0 > c) it = find_item(T, c, 0, it - 1);
     return factor == 1.f && T.item[it].src == T.item[it].dst;
@@ -352,16 +354,17 @@ prism_status check_tensors(const prism_tensor* t, int64_t n, bool writes) {
   return PRISM_OK;
 }
 
-// What one tensor's scaling writes may meet neither another tensor nor, other
-// than exactly, its own input.
-prism_status check_apart(const prism_tensor* t, int64_t n) {
+// What one tensor's scaling writes may meet neither another tensor nor the norm
+// nor, other than exactly, its own input.
+prism_status check_apart(const prism_tensor* t, int64_t n, const float* norm) {
   struct Range {
     uintptr_t a, e;
     bool written;
   };
   try {
     std::vector<Range> r;
-    r.reserve(size_t(n) * 2);
+    r.reserve(size_t(n) * 2 + 1);
+    r.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, false});
     for (int64_t i = 0; i < n; ++i) {
       if (!t[i].numel) continue;
       const uintptr_t bytes = uintptr_t(t[i].numel) * (t[i].dtype == PRISM_FP32 ? 4 : 2);
@@ -495,7 +498,7 @@ extern "C" prism_status prism_grad_scale(const prism_tensor* grads, int64_t n_te
                                          float max_norm, float eps, void* stream) {
   if (!norm || reinterpret_cast<uintptr_t>(norm) % 4 || bad_bound(max_norm, eps)) return PRISM_ERR_ARG;
   prism_status st = check_tensors(grads, n_tensors, true);
-  if (st == PRISM_OK) st = check_apart(grads, n_tensors);
+  if (st == PRISM_OK) st = check_apart(grads, n_tensors, norm);
   if (st != PRISM_OK) return st;
   GnScale g = {nullptr, 0, 0, const_cast<float*>(norm), 0, max_norm, eps};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -508,7 +511,7 @@ extern "C" prism_status prism_grad_clip(const prism_tensor* grads, int64_t n_ten
   if (ord != PRISM_NORM_L2 && ord != PRISM_NORM_INF) return PRISM_ERR_ARG;
   prism_status st = check_tensors(grads, n_tensors, true);
   if (st == PRISM_OK) st = check_norm_ws(ws, ws_bytes, n_tensors);
-  if (st == PRISM_OK) st = check_apart(grads, n_tensors);
+  if (st == PRISM_OK) st = check_apart(grads, n_tensors, norm);
   if (st != PRISM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   double* partial;

@@ -306,22 +306,29 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_staged_kernel(const __gr
     }
 }
 
-// Turns per position of pair j of an axis with n rotated channels.
-double pair_turns(const prism_rope_params& r, int n, int j) {
-  const double two_pi = 6.283185307179586476925286766559;
+// Turns per position of the pairs of an axis with n rotated channels. The
+// powers theta^(-2j/n) come one from the other in extended precision, exact to
+// fp64 for every j.
+void axis_turns(const prism_rope_params& r, int n, double* turns) {
+  const long double two_pi = 6.283185307179586476925286766559L;
   double theta = r.theta;
   if (r.scaling == PRISM_ROPE_NTK && n > 2) theta *= std::pow(r.factor, double(n) / (n - 2));
-  const double f = std::pow(theta, -2.0 * j / n);
-  double share = r.scaling == PRISM_ROPE_LINEAR ? 1.0 : 0.0;  // of the stretched frequency
+  // with YaRN, pairs that turn more than 32 times over the trained length keep their frequency, those below one turn
+  // are stretched, a ramp over the index between
+  double low = 0.0, width = 1.0;
   if (r.scaling == PRISM_ROPE_YARN) {
-    // pairs that turn more than 32 times over the trained length keep their
-    // frequency, those below one turn are stretched, a ramp over the index between
     const double per = n / (2.0 * std::log(theta));
-    const double low = std::fmax(std::floor(per * std::log(r.trained_len / (32.0 * two_pi))), 0.0);
-    const double high = std::fmin(std::ceil(per * std::log(r.trained_len / two_pi)), double(n - 1));
-    share = std::fmin(std::fmax((j - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+    low = std::fmax(std::floor(per * std::log(r.trained_len / (32.0 * double(two_pi)))), 0.0);
+    const double high = std::fmin(std::ceil(per * std::log(r.trained_len / double(two_pi))), double(n - 1));
+    width = std::fmax(high - low, 0.001);
   }
-  return (f / r.factor * share + f * (1.0 - share)) / two_pi;
+  const long double step = powl(theta, -2.0L / n);
+  long double f = 1.0L / two_pi;
+  for (int j = 0; j < n / 2; ++j, f *= step) {
+    double share = r.scaling == PRISM_ROPE_LINEAR ? 1.0 : 0.0;  // of the stretched frequency
+    if (r.scaling == PRISM_ROPE_YARN) share = std::fmin(std::fmax((j - low) / width, 0.0), 1.0);
+    turns[j] = share == 0.0 ? double(f) : double(f) / r.factor * share + double(f) * (1.0 - share);
+  }
 }
 
 prism_status check_rope(const prism_rope_params* r, int head_dim, int* rot) {
@@ -414,8 +421,9 @@ cudaError_t dispatch_staged(const RopeArgs& a, int ev, int smem, cudaStream_t s)
 
 // x modulo 1 in units of 2^-64 (its two's complement for a negative x).
 uint64_t fraction_bits(double x) {
-  const double r = std::fmod(x, 1.0);
-  const uint64_t b = uint64_t(std::ldexp(std::fabs(r), 64));  // below 2^64: fmod is exact
+  if (x == 0.0) return 0;
+  const double r = std::fabs(x) < 1.0 ? x : std::fmod(x, 1.0);  // exact
+  const uint64_t b = uint64_t(std::fabs(r) * 18446744073709551616.0);
   return r < 0.0 ? uint64_t(0) - b : b;
 }
 
@@ -477,6 +485,9 @@ extern "C" prism_status prism_rope(const prism_rope_params* params, const prism_
         return PRISM_ERR_ARG;
       if (v > w && rows_meet(d, a.dst_ld[w] * es, ww, reinterpret_cast<uintptr_t>(a.dst[v]), a.dst_ld[v] * es, wv, n_tokens))
         return PRISM_ERR_ARG;
+      if (positions && rows_meet(d, a.dst_ld[w] * es, ww, reinterpret_cast<uintptr_t>(positions),
+                                 int64_t(params->n_axes) * 4, int64_t(params->n_axes) * 4, n_tokens))
+        return PRISM_ERR_ARG;
     }
   a.n = n_tokens;
   a.pos = positions;
@@ -493,12 +504,15 @@ extern "C" prism_status prism_rope(const prism_rope_params* params, const prism_
   a.by_pairs = fast_div(a.pairs);
   a.m = float(params->magnitude);
   a.sign = transposed ? -1.f : 1.f;
-  for (int x = 0, i = 0; x < a.axes; ++x)
+  double turns[kRopeMaxPairs];
+  for (int x = 0, i = 0; x < a.axes; ++x) {
+    if (params->axis_dim[x] == 0) continue;
+    axis_turns(*params, params->axis_dim[x], turns);
     for (int j = 0; j < params->axis_dim[x] / 2; ++j, ++i) {
-      const double f = pair_turns(*params, params->axis_dim[x], j);
-      a.turn[i] = fraction_bits(params->pos_scale[x] * f);
-      a.start[i] = fraction_bits(params->pos_offset[x] * f);
+      a.turn[i] = fraction_bits(params->pos_scale[x] * turns[j]);
+      a.start[i] = fraction_bits(params->pos_offset[x] * turns[j]);
     }
+  }
   // the widest vector that divides the head, the half and every address and stride
   const bool half = params->layout == PRISM_ROPE_HALF;
   int ev = 16 / int(es);

@@ -199,6 +199,7 @@ def test_empty_streams_and_graphs():
     assert y.shape == (0, d) and g.shape == (0, f)
     dx, dwg, dwu, dwd = P.gated_ffn_bwd(dy[:0], x[:0], wg, wu, wd, g, u)
     assert dx.shape == (0, d) and all((t == 0).all() for t in (dwg, dwu, dwd))
+    assert P.gated_ffn_bwd(dy[:0], x[:0], wg, wu, wd, g, u, need_dw=False)[0].shape == (0, d)
     want = P.gated_ffn_fwd(x, wg, wu, wd)
     wantb = P.gated_ffn_bwd(dy, x, wg, wu, wd, want[1], want[2])
     # another stream, with no workspace given: its memory is not handed on before the stream is done with it

@@ -131,6 +131,28 @@ def test_nonfinite_and_empty():
 
 
 @pytest.mark.gpu
+def test_dense_in_any_order_and_zeros():
+    require_gpu()
+    g = [t.view(40, 30, 50) for t in tensors([60000, 60000], 12)]
+    turned = [g[0].permute(2, 0, 1), g[1].transpose(0, 2)]
+    ref = O.grad_norm([f64(t) for t in g])
+    norm = P.clip_grad_norm(turned, ref / 4)
+    assert abs(float(norm) - ref) <= NORM_TOL * ref
+    assert abs(O.grad_norm([f64(t) for t in g]) - ref / 4) <= 2.0 ** -8 * ref / 4
+    # zeros around one value, and values that a square loses in fp32
+    z = torch.zeros(100000, device="cuda")
+    z[777] = 3.0
+    assert float(P.grad_norm([z, torch.zeros_like(z)])) == 3.0
+    z[777] = 2.0 ** -100
+    assert float(P.grad_norm([z])) == 2.0 ** -100
+    z[777] = float("nan")
+    was = torch.arange(5.0, device="cuda")
+    keep = was.clone()
+    P.clip_grad_norm([z, was], math.inf)  # nothing to clip to: whatever the norm
+    assert torch.equal(was, keep)
+
+
+@pytest.mark.gpu
 def test_same_bits_stream_and_graph():
     require_gpu()
     g = tensors([1000003, 17, 250000], 7)
@@ -194,8 +216,11 @@ def test_refusals():
     b = ctypes.c_size_t()
     assert P.lib().prism_grad_norm_workspace_size(-1, ctypes.byref(b)) == 1
     assert P.lib().prism_grad_norm_workspace_size((1 << 20) + 1, ctypes.byref(b)) == 9
+    assert scale([((1 << 20), None, 100, 0, 0)]) == 1  # over the norm itself
     with pytest.raises(P.PrismError):
         P.GradList([torch.zeros(4, 4).t()[1:]])
+    with pytest.raises(P.PrismError):
+        P.GradList([torch.zeros(4, 6)], out=[torch.zeros(6, 4).t()])
     with pytest.raises(P.PrismError):
         P.GradList([torch.zeros(4)], out=[])
     with pytest.raises(P.PrismError):

@@ -245,6 +245,7 @@ def test_refusals():
     assert _call(qo=1 << 20, so=256) == 1
     assert _call(k=1 << 21, ko=1 << 22, hk=2, sk=128, sko=128) == 1
     assert _call(k=1 << 22, ko=(1 << 21) + 128, hk=2, sk=128, sko=128) == 1
+    assert _call(pos=(1 << 21) + 512) == 1  # the output over the positions
     assert _call(n=0) == 0
     for bad in (dict(layout="halves"), dict(scaling="other"), dict(pos_scale=(1.0, 2.0)),
                 dict(scaling="yarn", factor=0.0)):
