@@ -469,9 +469,10 @@ class _On:
     def __init__(self, tensors, stream, what):
         index = tensors[0].get_device()
         for t in tensors:
-            if t.get_device() != index or index < 0:
-                _require(t.get_device() >= 0, f"{what}: tensors must be on a CUDA device")
-                _require(False, f"{what}: tensors on different devices")
+            if t.get_device() != index:
+                _require(False, what + ": tensors on different devices")
+        if index < 0:
+            _require(False, what + ": tensors must be on a CUDA device")
         self.guard = None
         if index != torch._C._cuda_getDevice():
             self.guard = torch.cuda.device(index)
@@ -574,10 +575,10 @@ def _rope(q, k, spec, grid, positions, out, stream, transposed, what):
         pp = positions.data_ptr()
     with _On(tensors, stream, what) as on:
         if out is None:
-            oq = q.new_empty((n, hq, d))
+            oq = torch.empty_like(q) if q.is_contiguous() else q.new_empty(n, hq, d)
             soq = hq * d
             if k is not None:
-                ok = k.new_empty((n, hk, d))
+                ok = torch.empty_like(k) if k.is_contiguous() else k.new_empty(n, hk, d)
                 sok = hk * d
             on.made(oq, ok)
         else:
@@ -638,6 +639,11 @@ def _ffn_workspace(ws, m, f, backward, device):
     return (ws or Workspace(device, b.value)).ensure(b.value)
 
 
+def _new_like(t: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
+    """A contiguous [rows, cols] matrix of t's type; t has that shape."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(rows, cols)
+
+
 def _same_type(tensors, what):
     kind = tensors[0].dtype
     for t in tensors:
@@ -664,13 +670,13 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
         ws = _ffn_workspace(ws, m, f, 0, x.device)
         y, gate, up, gp, upp = out, None, None, None, None
         if out is None:
-            y = x.new_empty((m, d))
+            y = _new_like(x, m, d)
             sy = d
         else:
             sy = _row_stride(y, m, d, what, "out")
         if save:
-            gate = x.new_empty((m, f))
-            up = x.new_empty((m, f))
+            gate = x.new_empty(m, f)
+            up = x.new_empty(m, f)
             gp, upp = gate.data_ptr(), up.data_ptr()
         on.made(y, gate, up, ws.buf)
         _check(lib().prism_gated_ffn_fwd(ctypes.byref(w), m, _ACT[act], code, x.data_ptr(), sx, y.data_ptr(), sy, gp, upp,
@@ -698,12 +704,10 @@ def gated_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up:
         ws = _ffn_workspace(ws, m, f, 1, x.device)
         dx = dwg = dwu = dwd = xp = gp = upp = dp = None
         if need_dx:
-            dx = x.new_empty((m, d))
+            dx = _new_like(x, m, d)
             xp = dx.data_ptr()
         if need_dw:
-            dwg = x.new_empty((f, d))
-            dwu = x.new_empty((f, d))
-            dwd = x.new_empty((d, f))
+            dwg, dwu, dwd = _new_like(w_gate, f, d), _new_like(w_up, f, d), _new_like(w_down, d, f)
             gp, upp, dp = dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()
         on.made(dx, dwg, dwu, dwd, ws.buf)
         _check(lib().prism_gated_ffn_bwd(ctypes.byref(w), m, _ACT[act], code, dy.data_ptr(), sdy, x.data_ptr(), sx,
@@ -764,8 +768,12 @@ def _grad_list(grads, out=None) -> GradList:
 
 
 def _norm_call(grads, ws, device, stream, what):
-    device = grads.device or torch.device(device)
-    norm = torch.empty((), dtype=torch.float32, device=device)
+    if grads.device is None:
+        device = torch.device(device)
+        norm = torch.empty((), dtype=torch.float32, device=device)
+    else:
+        device = grads.device
+        norm = grads.grads[0].new_empty((), dtype=torch.float32)
     ws = (ws or Workspace(device)).ensure(grads.workspace_bytes)
     return norm, _On((norm,), stream, what), ws
 

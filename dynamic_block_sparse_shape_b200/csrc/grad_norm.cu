@@ -25,6 +25,12 @@
 // scaling 0.59 ms (3.6 GB moved; without the loads ahead 0.63; 3 to 8 CTAs per SM
 // and 2 to 8 vectors measured: 4 of each is within 2 % of the best on large lists,
 // more CTAs spill registers or crowd the memory system).
+//
+// Small lists (at most kSmallChunks chunks) take one launch: a cluster of CTAs
+// reads every value once into registers, the sums meet in distributed shared
+// memory, and the values are scaled from the registers. 40,001 fp32 values in 6
+// tensors: 4.7 us on the GPU like the two launches, and 2 us less of the host (10.3 for
+// the whole Python call, 12.3).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -283,6 +289,12 @@ struct GnScale {
   float max_norm, eps;
 };
 
+// A NaN norm makes every value NaN, unless there is nothing to clip to.
+__device__ __forceinline__ float clip_factor(const GnScale& S, double norm) {
+  const double f = double(S.max_norm) / (norm + double(S.eps));
+  return f >= 1.0 || isinf(S.max_norm) ? 1.f : float(f);
+}
+
 // Pass 2: the factor, and this CTA's chunks times it, last chunk first.
 template <int CAP>
 __global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) scale_kernel(const __grid_constant__ GnTable<CAP> T, const GnScale S) {
@@ -292,9 +304,7 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) scale_kernel(const _
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the norm pass, where this launch was let in beside its end
   const double norm = S.partial ? combine(S.partial, S.parts, S.inf_norm) : double(*S.norm);
   if (S.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *S.norm = float(norm);
-  const double f = double(S.max_norm) / (norm + double(S.eps));
-  // a NaN norm makes every value NaN, unless there is nothing to clip to
-  const float factor = f >= 1.0 || isinf(S.max_norm) ? 1.f : float(f);
+  const float factor = clip_factor(S, norm);
   auto skip = [&](int c) {  // nothing to do for chunk c; also finds its item
     if (T.item[it].chunk0 > c) it = find_item(T, c, 0, it - 1);
     return factor == 1.f && T.item[it].src == T.item[it].dst;
@@ -337,6 +347,62 @@ cudaError_t launch_behind(void (*kernel)(K...), int ctas, cudaStream_t s, const 
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The whole of a small list in one launch of one cluster: chunk c is CTA c mod
+// kSmallCtas's; with `scale` the values are scaled, else only the norm is
+// written. The order of the sums is the chunks' and the ranks': fixed.
+constexpr int kSmallCtas = 8, kSmallPer = 4, kSmallChunks = kSmallCtas * kSmallPer;
+
+__global__ void __cluster_dims__(kSmallCtas) __launch_bounds__(kGnThreads)
+    small_kernel(const __grid_constant__ GnTable<kFew> T, const GnScale S, const int scale) {
+  __shared__ double part;
+  GnPlace p[kSmallPer];
+  uint4 v[kSmallPer][kGnVecs];
+#pragma unroll
+  for (int i = 0; i < kSmallPer; ++i) {
+    const int c = int(blockIdx.x) + i * kSmallCtas;
+    if (c < T.chunks) {
+      p[i] = place(T, c, find_item(T, c, 0, T.items - 1));
+      load_chunk(p[i], v[i]);
+    }
+  }
+  double acc = 0.0;
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kSmallPer; ++i)
+    if (int(blockIdx.x) + i * kSmallCtas < T.chunks) {
+      if (T.inf_norm) top = max(top, p[i].fp32 ? Chunk<true>{v[i]}.max_bits() : Chunk<false>{v[i]}.max_bits());
+      else acc += p[i].fp32 ? Chunk<true>{v[i]}.sum_squares() : Chunk<false>{v[i]}.sum_squares();
+    }
+  const double mine = cta_reduce(T.inf_norm ? double(top) : acc, T.inf_norm);
+  if (threadIdx.x == 0) part = mine;
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  double norm = 0.0;
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(&part));
+#pragma unroll
+  for (int r = 0; r < kSmallCtas; ++r) {
+    double x;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f64 %0, [a];\n\t}"
+        : "=d"(x)
+        : "r"(at), "r"(r));
+    norm = T.inf_norm ? (x > norm ? x : norm) : norm + x;
+  }
+  // every part is read before any CTA leaves
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  norm = T.inf_norm ? double(__uint_as_float(uint32_t(norm))) : sqrt(norm);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *S.norm = float(norm);
+  if (scale) {
+    const float factor = clip_factor(S, norm);
+#pragma unroll
+    for (int i = 0; i < kSmallPer; ++i)
+      if (int(blockIdx.x) + i * kSmallCtas < T.chunks && !(factor == 1.f && p[i].delta == 0)) {
+        if (p[i].fp32) Chunk<true>{v[i]}.store_scaled(factor, p[i]);
+        else Chunk<false>{v[i]}.store_scaled(factor, p[i]);
+      }
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 prism_status check_tensors(const prism_tensor* t, int64_t n, bool writes) {
@@ -386,6 +452,11 @@ prism_status check_apart(const prism_tensor* t, int64_t n, const float* norm) {
   return PRISM_OK;
 }
 
+int64_t chunks_of(const prism_tensor& t) {
+  const int64_t bytes = t.numel * (t.dtype == PRISM_FP32 ? 4 : 2) + int64_t(reinterpret_cast<uintptr_t>(t.data) % 16);
+  return (bytes + kGnChunkVecs * 16 - 1) / (kGnChunkVecs * 16);
+}
+
 // Launches of at most CAP tensors each; F(table, grid, first partial).
 template <int CAP, typename F>
 prism_status each_launch(const prism_tensor* t, int64_t n, bool inf_norm, const F& run) {
@@ -398,9 +469,7 @@ prism_status each_launch(const prism_tensor* t, int64_t n, bool inf_norm, const 
     int64_t chunks = 0;
     for (; i < n && T.items < CAP; ++i) {
       if (!t[i].numel) continue;
-      const int64_t bytes = t[i].numel * (t[i].dtype == PRISM_FP32 ? 4 : 2) +
-                            int64_t(reinterpret_cast<uintptr_t>(t[i].data) % 16);
-      const int64_t c = (bytes + kGnChunkVecs * 16 - 1) / (kGnChunkVecs * 16);
+      const int64_t c = chunks_of(t[i]);
       if (chunks + c > (int64_t(1) << 30)) {
         if (T.items == 0) return PRISM_ERR_UNSUPPORTED;
         break;
@@ -421,6 +490,21 @@ prism_status each_launch(const prism_tensor* t, int64_t n, bool inf_norm, const 
     parts += int(ctas);
   }
   return PRISM_OK;
+}
+
+// A small list in one launch; false when it is none.
+bool run_small(const prism_tensor* t, int64_t n, const GnScale& g, int scale, cudaStream_t s, prism_status* st) {
+  if (n > kFew) return false;
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < n && chunks <= kSmallChunks; ++i)
+    if (t[i].numel > kSmallChunks * kGnChunkVecs * 8) return false;
+    else if (t[i].numel) chunks += chunks_of(t[i]);
+  if (chunks == 0 || chunks > kSmallChunks) return false;
+  *st = each_launch<kFew>(t, n, g.inf_norm, [&](const GnTable<kFew>& T, int, int) {
+    small_kernel<<<kSmallCtas, kGnThreads, 0, s>>>(T, g, scale);
+    return cudaGetLastError();
+  });
+  return true;
 }
 
 size_t norm_ws_bytes(int64_t n) {
@@ -487,6 +571,8 @@ extern "C" prism_status prism_grad_norm(const prism_tensor* grads, int64_t n_ten
   if (st == PRISM_OK) st = check_norm_ws(ws, ws_bytes, n_tensors);
   if (st != PRISM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const GnScale small = {nullptr, 0, ord == PRISM_NORM_INF, norm, 1, 0.f, 0.f};
+  if (run_small(grads, n_tensors, small, 0, s, &st)) return st;
   double* partial;
   int parts;
   st = norm_parts(grads, n_tensors, ord, ws, &partial, &parts, s);
@@ -514,6 +600,8 @@ extern "C" prism_status prism_grad_clip(const prism_tensor* grads, int64_t n_ten
   if (st == PRISM_OK) st = check_apart(grads, n_tensors, norm);
   if (st != PRISM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const GnScale small = {nullptr, 0, ord == PRISM_NORM_INF, norm, 1, max_norm, eps};
+  if (run_small(grads, n_tensors, small, 1, s, &st)) return st;
   double* partial;
   int parts;
   st = norm_parts(grads, n_tensors, ord, ws, &partial, &parts, s);
