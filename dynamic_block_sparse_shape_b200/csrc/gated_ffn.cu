@@ -11,7 +11,10 @@
 // stays in tensor memory and becomes dg, du (and h again, from the saved
 // projections, so the forward need not keep it) in the epilogue; dx is one
 // product over both halves of K; the three weight gradients share a launch.
-// dg, du and h are rounded to bf16 once each, as operands of the next product.
+// dg, du and h are rounded to bf16 once each, as operands of the next product;
+// of at most kFineTokens tokens they carry their remainders along (twice the rows,
+// or a second segment of K, where the weights' bytes are the cost), so that every
+// output is rounded once.
 // Tensor operations: 6 M D F forward, 12 M D F backward; gemm.cuh says what
 // bounds the products.
 #include "gated_ffn.h"
@@ -19,9 +22,13 @@
 namespace prism {
 namespace {
 
-// Workspace: the status word, then h (forward), or dg, du, h (backward).
+// Workspace: the status word, then h (forward), or dg, du, h (backward): [m, f]
+// bf16, of few tokens [2 m, f] with the remainders behind.
+size_t ffn_part_bytes(int64_t m, int64_t f) {
+  return align_up(size_t(m) * size_t(f) * (m <= kFineTokens ? 4 : 2), 256);
+}
 size_t ffn_ws_bytes(int64_t m, int64_t f, bool backward) {
-  return kWsHeader + size_t(backward ? 3 : 1) * align_up(size_t(m) * size_t(f) * 2, 256);
+  return kWsHeader + size_t(backward ? 3 : 1) * ffn_part_bytes(m, f);
 }
 
 struct Rows {
@@ -109,13 +116,18 @@ extern "C" prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t 
   g.out[1] = {gate, f};
   g.out[2] = {up, f};
   g.m = m; g.n = f; g.k[0] = d;
+  const bool fine = m <= kFineTokens;
+  P.fine = fine;
   if ((st = ffn_gate_product(act, P, g, s)) != PRISM_OK) return st;
   GemmProblem r;
   r.a[0] = {h, f};
   r.b[0] = {w->w_down, w->down_stride};
   r.out[0] = {y, y_stride};
-  r.m = m; r.n = d; r.k[0] = f;
+  r.m = fine ? 2 * m : m;  // the values' rows, then the remainders': added to one another at the end
+  r.n = d; r.k[0] = f;
   P.follows = 1;
+  P.fine = 0;
+  P.fold = fine ? int(m) : 0;
   return ffn_product_nt(P, r, s);
 }
 
@@ -161,7 +173,8 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
       if (p && cudaMemsetAsync(p, 0, size_t(d) * f * 2, s) != cudaSuccess) return PRISM_ERR_CUDA;
     return PRISM_OK;
   }
-  const size_t part = align_up(size_t(m) * f * 2, 256);
+  const size_t part = ffn_part_bytes(m, f);
+  const bool fine = m <= kFineTokens;
   uint8_t* base = static_cast<uint8_t*>(ws) + kWsHeader;
   void *dg = base, *du = base + part, *h = base + 2 * part;
   GemmArgs P;
@@ -177,8 +190,10 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
   g.out[1] = {du, f};
   g.out[2] = {h, f};
   g.m = m; g.n = f; g.k[0] = d;
+  P.fine = fine;
   if ((st = ffn_gate_bwd_product(act, P, g, s)) != PRISM_OK) return st;
   P.follows = 1;
+  P.fine = 0;
   if (dx) {
     GemmProblem r;
     r.a[0] = {dg, f};
@@ -186,8 +201,11 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
     r.b[0] = {w->w_gate, w->gate_stride};
     r.b[1] = {w->w_up, w->up_stride};
     r.out[0] = {dx, dx_stride};
-    r.m = m; r.n = d; r.k[0] = f; r.k[1] = f;
+    r.m = fine ? 2 * m : m;  // folded as in the forward
+    r.n = d; r.k[0] = f; r.k[1] = f;
+    P.fold = fine ? int(m) : 0;
     if ((st = ffn_product_nn(P, r, s)) != PRISM_OK) return st;
+    P.fold = 0;
   }
   if (dw) {
     GemmProblem r[3];
@@ -200,6 +218,14 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
       r[i].m = i < 2 ? f : d;
       r[i].n = i < 2 ? d : f;
       r[i].k[0] = m;
+      if (fine) {  // the remainders as a second segment of K
+        const int64_t below = m * f;
+        r[i].a[1] = r[i].a[0];
+        r[i].b[1] = r[i].b[0];
+        GemmOperand& o2 = i < 2 ? r[i].a[1] : r[i].b[1];
+        o2.base = static_cast<const __nv_bfloat16*>(o2.base) + below;
+        r[i].k[1] = m;
+      }
     }
     if ((st = ffn_products_tn(P, r, 3, s)) != PRISM_OK) return st;
   }

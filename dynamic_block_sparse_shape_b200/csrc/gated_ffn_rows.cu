@@ -11,10 +11,14 @@
 // are four pairs of k, and since the sum over k may go in any order, the pairs go
 // into the instruction as they lie: tokens are read with the same permutation,
 // and no value moves between lanes. Sums stay in fp32 and are added over the
-// warps in shared memory in a fixed order.
-// 2048 x 5632, cold weights: one token 18.2 us, 8 tokens 19.0, 16 23.2, 32 26.8 in
-// both launches (the tiles of the split kernel: 29 to 31; multiply-adds on the
-// ordinary cores: 18.8 for one token, 45 for 8).
+// warps in shared memory in a fixed order. The gate product leaves h as m rows of
+// bf16 values and m rows of their bf16 remainders; the down product takes them as
+// 2 m tokens and adds the two, so y is rounded once and not on top of a rounded h.
+// 2048 x 5632, cold weights: 1 and 4 tokens 18.3 us, 8 tokens 20.8, 16 24.0 in both
+// launches (the tiles of the split kernel: 29 to 31; multiply-adds on the ordinary
+// cores: 18.8 for one token, 45 for 8). h rounded to bf16 instead: 18.2 for one
+// token, 19.0 for 8, 23.2 for 16, with 1.41 times the error of y; h in fp32, split
+// as it is read: 20.3 and 29.4 for 1 and 16.
 // The down product's first weights are requested before it waits for h
 // (programmatic dependent launch): they do not depend on it.
 #include "gated_ffn.h"
@@ -27,11 +31,11 @@ constexpr int kRowTile = 16;   // weight rows of a product
 struct RowArgs {
   const __nv_bfloat16* w[2];  // gate: Wg, Wu; down: Wd
   int64_t w_ld[2];
-  const __nv_bfloat16* x;  // [m, k]
+  const __nv_bfloat16* x;  // [m, k]; down: h, [2 m, k]
   int64_t x_ld;
   __nv_bfloat16* out[3];  // gate: h, g, u; down: y
-  int64_t out_ld[3];
-  int m, rows, k;  // rows: f or d
+  int64_t out_ld;
+  int m, rows, k;  // m: tokens of x (down: 2 m); rows: f or d
   int save;
 };
 
@@ -112,21 +116,25 @@ __global__ void __launch_bounds__(row_warps(GATE) * 32) rows_kernel(const RowArg
   __syncthreads();
   for (int x = threadIdx.x; x < kRowTile * NT * 8; x += kRowWarps * 32) {
     const int r = x % kRowTile, m = x / kRowTile, f = f0 + r;
-    if (f >= P.rows || m >= P.m) continue;
+    const int tokens = GATE ? P.m : P.m / 2;
+    if (f >= P.rows || m >= tokens) continue;
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int v = 0; v < kRowWarps; ++v) {
       a += part[v][r][m];
-      if constexpr (GATE) b += part[v][r + kRowTile][m];
+      b += GATE ? part[v][r + kRowTile][m] : part[v][r][m + tokens];
     }
     if constexpr (GATE) {
-      P.out[0][m * P.out_ld[0] + f] = __float2bfloat16_rn(act_f<ACT>(a) * b);
+      const float h = act_f<ACT>(a) * b;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+      P.out[0][m * P.out_ld + f] = hi;
+      P.out[0][(m + P.m) * P.out_ld + f] = __float2bfloat16_rn(remainder_bf16(h, __bfloat162float(hi)));
       if (P.save) {
-        P.out[1][m * P.out_ld[1] + f] = __float2bfloat16_rn(a);
-        P.out[2][m * P.out_ld[2] + f] = __float2bfloat16_rn(b);
+        P.out[1][m * P.out_ld + f] = __float2bfloat16_rn(a);
+        P.out[2][m * P.out_ld + f] = __float2bfloat16_rn(b);
       }
     } else {
-      P.out[0][m * P.out_ld[0] + f] = __float2bfloat16_rn(a);
+      P.out[0][m * P.out_ld + f] = __float2bfloat16_rn(a + b);
     }
   }
 }
@@ -160,8 +168,11 @@ prism_status launch_rows(const RowArgs& a, bool follows, cudaStream_t s) {
 template <bool GATE, int ACT>
 prism_status rows_for(const RowArgs& a, bool follows, cudaStream_t s) {
   if (a.m <= 8) return launch_rows<1, GATE, ACT>(a, follows, s);
-  if (a.m <= 16) return launch_rows<2, GATE, ACT>(a, follows, s);
-  return launch_rows<4, GATE, ACT>(a, follows, s);
+  static_assert(kRowTokens == 16, "two groups of tokens, four of h");
+  if constexpr (!GATE) {
+    if (a.m > 16) return launch_rows<4, GATE, ACT>(a, follows, s);
+  }
+  return launch_rows<2, GATE, ACT>(a, follows, s);
 }
 
 }  // namespace
@@ -177,11 +188,10 @@ prism_status ffn_rows_forward(int act, const prism_ffn_weights& w, int m, const 
   a.w_ld[1] = w.up_stride;
   a.x = static_cast<const B*>(x);
   a.x_ld = x_ld;
-  void* out[3] = {h, gate, up};
-  for (int i = 0; i < 3; ++i) {
-    a.out[i] = static_cast<B*>(out[i]);
-    a.out_ld[i] = w.f;
-  }
+  a.out[0] = static_cast<B*>(h);
+  a.out[1] = static_cast<B*>(gate);
+  a.out[2] = static_cast<B*>(up);
+  a.out_ld = w.f;
   a.m = m; a.rows = w.f; a.k = w.d;
   a.save = gate != nullptr;
   prism_status st;
@@ -197,8 +207,8 @@ prism_status ffn_rows_forward(int act, const prism_ffn_weights& w, int m, const 
   a.x = static_cast<const B*>(h);
   a.x_ld = w.f;
   a.out[0] = static_cast<B*>(y);
-  a.out_ld[0] = y_ld;
-  a.rows = w.d; a.k = w.f;
+  a.out_ld = y_ld;
+  a.m = 2 * m; a.rows = w.d; a.k = w.f;
   return rows_for<false, PRISM_ACT_SILU>(a, true, s);
 }
 

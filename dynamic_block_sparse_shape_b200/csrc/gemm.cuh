@@ -69,6 +69,9 @@ struct GemmArgs {
   int whole, units;   // tiles taken whole; these and the halves of the others
   int save;
   int follows;        // launched behind another product of the same call
+  // split kernel of single CTAs alone: kEpiGate (h) and kEpiGateBwd also write the bf16 remainders, m rows further on
+  // (`fine`); kEpiStore adds row r + fold to row r and has `fold` rows
+  int fine, fold;
   int* status;
 };
 
@@ -103,6 +106,11 @@ struct GemmLayout {
   static_assert(kSmem <= kGemmMaxSmem && kStages >= 3, "shared memory");
   static_assert(kCols <= 512, "tensor memory");
 };
+
+// What rounding v to the bf16 value `hi` left over (nothing of an infinity or NaN).
+__device__ __forceinline__ float remainder_bf16(float v, float hi) {
+  return fabsf(hi) < __int_as_float(0x7f800000) ? v - hi : 0.f;
+}
 
 // ---------------------------------------------------------------- activations
 // With e = exp(-z), sigmoid(z) = 1 / (1 + e) keeps its relative precision on

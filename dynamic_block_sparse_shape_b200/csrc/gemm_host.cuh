@@ -130,6 +130,8 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
   std::memset(&A, 0, sizeof(A));
   A.products = products;
   A.save = P.save;
+  A.fine = P.fine;
+  A.fold = P.fold;
   A.status = P.status;
   const int a_rows = AMN || CG == 2 || pr[0].m >= kGemmM ? kGemmM : int(pr[0].m + 7) / 8 * 8;
   A.a_bytes = a_rows * 128;
@@ -199,9 +201,9 @@ struct GemmChoice {
 // The kernel and tiles for products of m x n rows each (n: columns of the
 // accumulator): the choice of least time by the figures above; what they are
 // off by shows only where two choices are close. `sub`: accumulators of a tile
-// of the pair kernel.
+// of the pair kernel; `single`: single CTAs only (what the pairs' epilogue lacks).
 inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, int64_t slices, bool a_mn, int sub,
-                              bool ragged) {
+                              bool ragged, bool single) {
   const int sms = device_sm_count();
   auto tiles = [&](int64_t rows, int64_t cols) {
     double t = 0;
@@ -216,8 +218,10 @@ inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, 
   const double both = sub == 1 ? one : std::fmax(49152.0 / rate, 1024 * kCycleNs);
   double best = k * (whole * both + (rest > 0 ? (rest * 2 <= pairs ? one : both) : 0.0)) + kTileNs;
   GemmChoice c = {2, 0, 1};
+  if (single) best = HUGE_VAL;
   const GemmChoice tries[] = {{1, 64, 8}, {1, 128, 4}, {2, 256, 4}};  // with the most parts
   for (const GemmChoice& t : tries) {
+    if (single && t.cg == 2) continue;
     const int rows_a = a_mn || t.cg == 2 || m[0] >= kGemmM ? kGemmM : int(m[0] + 7) / 8 * 8;
     const double bytes = (rows_a + t.bn / t.cg) * 128.0;
     for (int parts = 1; parts <= t.parts && parts <= slices; parts *= 2) {
@@ -256,7 +260,7 @@ prism_status gemm(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t
     slices = std::max(slices, (pr[i].k[0] + kGemmK - 1) / kGemmK + (pr[i].k[1] + kGemmK - 1) / kGemmK);
     ragged = ragged || pr[i].a[0].ld % 64 || pr[i].b[0].ld % 64;
   }
-  const GemmChoice c = gemm_choice(m, n, products, slices, AMN, kSub, ragged);
+  const GemmChoice c = gemm_choice(m, n, products, slices, AMN, kSub, ragged, P.fine || P.fold);
   if (c.bn == 0) return gemm_launch<2, 256, kSub, AMN, BMN, EPI, ACT>(P, pr, products, s);
   if (c.cg == 1 && c.bn == 64) return gemm_split_launch<1, 64, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);
   if (c.cg == 1) return gemm_split_launch<1, 128, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);

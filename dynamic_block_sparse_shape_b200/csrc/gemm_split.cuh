@@ -34,7 +34,7 @@ struct SplitArgs {
 
 struct SplitLaunch {
   SplitArgs p[kGemmProducts];
-  int products, save;
+  int products, save, fine, fold;  // see GemmArgs
   int a_bytes, stages;  // of A's part of a slice, and slices of the ring
   int* status;
 };
@@ -84,6 +84,19 @@ __device__ __forceinline__ void sum_parts(uint32_t at, int parts, uint32_t cta, 
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+// 8 values to `to`, rounded, and with `fine` their remainders `below` elements further on.
+__device__ __forceinline__ void store8(__nv_bfloat16* to, const float* v, bool fine, int64_t below) {
+  const uint4 h = pack8(v);
+  *reinterpret_cast<uint4*>(to) = h;
+  if (fine) {
+    const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      r[i] = remainder_bf16(v[i], __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16));
+    *reinterpret_cast<uint4*>(to + below) = pack8(r);
+  }
 }
 __device__ __forceinline__ void unpack8(const uint4& u, float* v) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -242,7 +255,8 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
   const int vecs = (min(kCols, Q.n - col0) + 7) / 8;  // n is a multiple of 8
   const int v0 = vecs * part_of / parts, mine = vecs * (part_of + 1) / parts - v0;
   if (!gave_up && mine > 0) {
-    for (int x = threadIdx.x; x < rows * mine; x += kGemmThreads) {
+    const int out_rows = EPI == kEpiStore && P.fold ? P.fold : rows;
+    for (int x = threadIdx.x; x < out_rows * mine; x += kGemmThreads) {
       const int r = x / mine, v = v0 + x - r * mine;
       const uint32_t at = smem_u32(part + r * kPitch + 8 * v);
       const int64_t row = row0 + r;
@@ -250,13 +264,19 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
       float d[8];
       sum_parts<CG>(at, parts, cta, d);
       if constexpr (EPI == kEpiStore) {
+        if (P.fold) {
+          float e[8];
+          sum_parts<CG>(at + P.fold * kPitch * 4, parts, cta, e);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] += e[i];
+        }
         *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(d);
       } else if constexpr (EPI == kEpiGate) {
         float u[8], h[8];
         sum_parts<CG>(at + BN / 2 * 4, parts, cta, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = act_f<ACT>(d[i]) * u[i];
-        *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(h);
+        store8(Q.out[0] + row * Q.out_ld[0] + col, h, P.fine, Q.m * Q.out_ld[0]);
         if (P.save) {
           *reinterpret_cast<uint4*>(Q.out[1] + row * Q.out_ld[1] + col) = pack8(d);
           *reinterpret_cast<uint4*>(Q.out[2] + row * Q.out_ld[2] + col) = pack8(u);
@@ -273,9 +293,9 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
           du[i] = d[i] * a;
           h[i] = a * u[i];
         }
-        *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(dg);
-        *reinterpret_cast<uint4*>(Q.out[1] + row * Q.out_ld[1] + col) = pack8(du);
-        if (P.save) *reinterpret_cast<uint4*>(Q.out[2] + row * Q.out_ld[2] + col) = pack8(h);
+        store8(Q.out[0] + row * Q.out_ld[0] + col, dg, P.fine, Q.m * Q.out_ld[0]);
+        store8(Q.out[1] + row * Q.out_ld[1] + col, du, P.fine, Q.m * Q.out_ld[1]);
+        if (P.save) store8(Q.out[2] + row * Q.out_ld[2] + col, h, P.fine, Q.m * Q.out_ld[2]);
       }
     }
   }

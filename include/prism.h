@@ -563,7 +563,9 @@ typedef struct {
  * gate, up: device [m, f] contiguous outs, or both NULL: the projections
  *       x w_gate^T and x w_up^T, rounded, for the backward pass.
  * Products accumulate in fp32; h = act(gate) * up is formed from the unrounded
- * projections and rounded to bf16 once, as an operand of the second product.
+ * projections and rounded to bf16 once, as an operand of the second product (of
+ * at most 32 tokens it is kept to 16 bits and more, as two operands: an infinite
+ * weight or input may then give NaN where one operand gives an infinity).
  * No output may share memory with gate, up or the weights; y may be x.
  * ws: at least prism_gated_ffn_workspace_size(m, f, 0) bytes (the status word
  *       and h).
@@ -575,8 +577,9 @@ PRISM_API prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t m
 /*
  * Gradient of prism_gated_ffn_fwd at the saved projections gate, up [m, f]
  * (contiguous): with dh = dy w_down, dg = dh up act'(gate), du = dh act(gate)
- * (each rounded to bf16 once): dx = dg w_gate + du w_up, dw_gate = dg^T x,
- * dw_up = du^T x, dw_down = dy^T (act(gate) up). relu'(0) = 0.
+ * (each rounded to bf16 once, or of at most 32 tokens kept to 16 bits and more):
+ * dx = dg w_gate + du w_up, dw_gate = dg^T x, dw_up = du^T x,
+ * dw_down = dy^T (act(gate) up). relu'(0) = 0.
  * dx: device [m, d] out, or NULL. dw_gate, dw_up [f, d], dw_down [d, f]: device
  *       contiguous outs, or all NULL (frozen weights). m = 0 zeroes them.
  * No output may share memory with any other tensor of the call.
