@@ -227,6 +227,7 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
         r[i].k[1] = m;
       }
     }
+    P.beside = dx != nullptr;
     if ((st = ffn_products_tn(P, r, 3, s)) != PRISM_OK) return st;
   }
   return PRISM_OK;

@@ -69,6 +69,9 @@ struct GemmArgs {
   int whole, units;   // tiles taken whole; these and the halves of the others
   int save;
   int follows;        // launched behind another product of the same call
+  // reads nothing of the product it follows, which itself waited for all that both read before it let this one start:
+  // runs beside it, and waits for it at the end alone, so that what comes next finds both complete
+  int beside;
   // split kernel of single CTAs alone: kEpiGate (h) and kEpiGateBwd also write the bf16 remainders, m rows further on
   // (`fine`); kEpiStore adds row r + fold to row r and has `fold` rows
   int fine, fold;
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   else __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  grid_dependency_wait();
+  if (!P.beside) grid_dependency_wait();
   grid_launch_dependents();
 
   if (warp == 0) {
@@ -668,6 +671,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     tmem_dealloc_cg<CG>(tbase, L::kCols);
   }
   if constexpr (CG == 2) cluster_sync_all();
+  if (P.beside) grid_dependency_wait();
 }
 
 }  // namespace prism

@@ -130,6 +130,7 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
   std::memset(&A, 0, sizeof(A));
   A.products = products;
   A.save = P.save;
+  A.beside = P.beside;
   A.fine = P.fine;
   A.fold = P.fold;
   A.status = P.status;

@@ -34,7 +34,7 @@ struct SplitArgs {
 
 struct SplitLaunch {
   SplitArgs p[kGemmProducts];
-  int products, save, fine, fold;  // see GemmArgs
+  int products, save, beside, fine, fold;  // see GemmArgs
   int a_bytes, stages;  // of A's part of a slice, and slices of the ring
   int* status;
 };
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
 
-  grid_dependency_wait();
+  if (!P.beside) grid_dependency_wait();
   grid_launch_dependents();
 
   if (warp == 0) {
@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
     tc_fence_after();
     tmem_dealloc_cg<CG>(tbase, BN);
   }
+  if (P.beside) grid_dependency_wait();
 }
 
 }  // namespace prism
