@@ -103,7 +103,7 @@ extern "C" prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t 
   if (m == 0) return PRISM_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void* h = static_cast<uint8_t*>(ws) + kWsHeader;
-  if (m <= kRowTokens) return ffn_rows_forward(act, *w, int(m), x, x_stride, h, y, y_stride, gate, up, s);
+  if (ffn_takes_rows(m, d)) return ffn_rows_forward(act, *w, int(m), x, x_stride, h, y, y_stride, gate, up, s);
   GemmArgs P;
   std::memset(&P, 0, sizeof(P));
   P.status = ws_status(ws);

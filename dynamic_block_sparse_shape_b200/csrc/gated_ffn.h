@@ -13,10 +13,10 @@ prism_status ffn_gate_bwd_product(int act, GemmArgs& P, const GemmProblem& pr, c
 prism_status ffn_product_nt(GemmArgs& P, const GemmProblem& pr, cudaStream_t s);
 prism_status ffn_product_nn(GemmArgs& P, const GemmProblem& pr, cudaStream_t s);
 // Of at most kFineTokens tokens h, dg and du are held as bf16 values and, m rows
-// further on, their bf16 remainders: the weights' bytes are the cost there. At
-// most kRowTokens go through the weights' rows forward.
-constexpr int kFineTokens = 32, kRowTokens = 16;
-// the whole forward pass of at most kRowTokens tokens, y = x allowed; h: [2 m, f]
+// further on, their bf16 remainders: the weights' bytes are the cost there.
+constexpr int kFineTokens = 32;
+// the whole forward pass of a handful of tokens, y = x allowed; h: [2 m, f]
+bool ffn_takes_rows(int64_t m, int d);
 prism_status ffn_rows_forward(int act, const prism_ffn_weights& w, int m, const void* x, int64_t x_ld, void* h, void* y,
                               int64_t y_ld, void* gate, void* up, cudaStream_t s);
 prism_status ffn_products_tn(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s);

@@ -48,13 +48,9 @@ __device__ __forceinline__ void mma_rows(float* c, uint32_t a0, uint32_t a1, uin
 }
 
 // NT: groups of 8 tokens; U: steps of 32 values of K whose loads go together.
-// The gate product has twice the rows: few warps a CTA, several CTAs an SM.
-// The down product has few rows and a long K: many warps share them.
-constexpr int row_warps(bool gate) { return gate ? 4 : 16; }
-
-template <int NT, bool GATE, int ACT, int U>
-__global__ void __launch_bounds__(row_warps(GATE) * 32) rows_kernel(const RowArgs P) {
-  constexpr int kRowWarps = row_warps(GATE), kU = U, kRowBlock = 32 * U;
+template <int NT, bool GATE, int ACT, int U, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) rows_kernel(const RowArgs P) {
+  constexpr int kRowWarps = WARPS, kU = U, kRowBlock = 32 * U;
   constexpr int kT = GATE ? 2 : 1;  // weight tiles
   __shared__ float part[kRowWarps][kT * kRowTile][NT * 8 + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,43 +135,56 @@ __global__ void __launch_bounds__(row_warps(GATE) * 32) rows_kernel(const RowArg
   }
 }
 
-template <int NT, bool GATE, int ACT, int U>
+template <int NT, bool GATE, int ACT, int U, int WARPS>
 prism_status launch_rows_as(const RowArgs& a, bool follows, cudaStream_t s) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((a.rows + kRowTile - 1) / kRowTile);
-  cfg.blockDim = dim3(row_warps(GATE) * 32);
+  cfg.blockDim = dim3(WARPS * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = follows ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, rows_kernel<NT, GATE, ACT, U>, a));
+  return cuda_status(cudaLaunchKernelEx(&cfg, rows_kernel<NT, GATE, ACT, U, WARPS>, a));
 }
 
-// The down product of a small layer has a CTA per SM at most: 128 values at a
-// time keep more loads in flight (2048 x 5632, one token: 9.8 us, 13.0 with 64);
-// with more CTAs their registers count (4096 x 11264: 26.5 us, 22.7 with 64).
+// With a CTA per SM at most, K is shared by 16 warps, else by 4 that leave the SM
+// room for other CTAs (the gate product of 1024 values of f, d = 4096: 11.2 us the
+// call, 18.3 with 4). The down product has few rows and a long K: always 16, and
+// with a CTA per SM at most 128 values at a time keep more loads in flight (2048 x
+// 5632, one token: 9.8 us, 13.0 with 64); with more CTAs their registers count
+// (4096 x 11264: 26.5 us, 22.7 with 64).
 template <int NT, bool GATE, int ACT>
 prism_status launch_rows(const RowArgs& a, bool follows, cudaStream_t s) {
-  if constexpr (!GATE) {
-    if ((a.rows + kRowTile - 1) / kRowTile <= device_sm_count()) return launch_rows_as<NT, GATE, ACT, 4>(a, follows, s);
+  const bool few = (a.rows + kRowTile - 1) / kRowTile <= device_sm_count();
+  if constexpr (GATE) {
+    if (!few) return launch_rows_as<NT, GATE, ACT, 2, 4>(a, follows, s);
+  } else {
+    if (few) return launch_rows_as<NT, GATE, ACT, 4, 16>(a, follows, s);
   }
-  return launch_rows_as<NT, GATE, ACT, 2>(a, follows, s);
+  return launch_rows_as<NT, GATE, ACT, 2, 16>(a, follows, s);
 }
 
 template <bool GATE, int ACT>
 prism_status rows_for(const RowArgs& a, bool follows, cudaStream_t s) {
   if (a.m <= 8) return launch_rows<1, GATE, ACT>(a, follows, s);
-  static_assert(kRowTokens == 16, "two groups of tokens, four of h");
   if constexpr (!GATE) {
-    if (a.m > 16) return launch_rows<4, GATE, ACT>(a, follows, s);
+    // few weight rows alone: see ffn_takes_rows
+    if (a.m > 16) return launch_rows_as<4, GATE, ACT, 4, 16>(a, follows, s);
   }
   return launch_rows<2, GATE, ACT>(a, follows, s);
 }
 
 }  // namespace
+
+// Up to 8 tokens, and up to 16 where a CTA per SM at most takes the down product:
+// each reads all of h, by then more than its weights. 16 tokens, this way / by
+// tiles: 2048 x 5632 24.0 / 30.8 us, 2368 x 6400 29.0 / 33.2, 2384 x 6400 49.4 /
+// 34.2, 4096 x 11264 104 / 61.6; 8 tokens: 4096 x 11264 50 / 60, 8192 x 22528
+// 185 / 209.
+bool ffn_takes_rows(int64_t m, int d) { return m <= 8 || (m <= 16 && (d + kRowTile - 1) / kRowTile <= device_sm_count()); }
 
 prism_status ffn_rows_forward(int act, const prism_ffn_weights& w, int m, const void* x, int64_t x_ld, void* h, void* y,
                               int64_t y_ld, void* gate, void* up, cudaStream_t s) {

@@ -81,8 +81,9 @@ def check_bwd(dy, x, wg, wu, wd, gate, up, act, got):
 
 # one token, single rows past a tile, widths of 8 values, K of less than a slice, sizes that give pairs of CTAs for
 # every product
-SIZES = [(1, 8, 8), (1, 64, 128), (2, 72, 136), (3, 520, 264), (8, 2312, 40), (5, 40, 2312), (31, 256, 64), (32, 1096, 200), (33, 200, 1096), (12, 72, 5000), (127, 64, 192), (128, 256, 256), (129, 264, 520),
-         (300, 1160, 392), (1000, 136, 2056)]
+SIZES = [(1, 8, 8), (1, 64, 128), (2, 72, 136), (3, 520, 264), (8, 2312, 40), (5, 40, 2312), (31, 256, 64),
+         (32, 1096, 200), (33, 200, 1096), (12, 72, 5000), (127, 64, 192), (128, 256, 256), (129, 264, 520),
+         (300, 1160, 392), (1000, 136, 2056), (7, 2400, 136), (16, 2368, 136), (9, 2400, 72), (17, 72, 72)]
 LARGE = [(700, 1160, 1032), (300, 2312, 1032), (2100, 2312, 2056), (2305, 2304, 1288), (4700, 40, 2056), (9000, 264, 1032)]
 
 
