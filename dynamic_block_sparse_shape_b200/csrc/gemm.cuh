@@ -11,13 +11,19 @@
 // three weight gradients).
 //
 // Tiles. What the tensor cores can be fed from L2 decides (measured: about 55
-// bytes per cycle and SM at 1.5 GHz). CG = 2: a pair of CTAs on neighbouring SMs
+// bytes per cycle and SM at 1.5 GHz). A pair of CTAs on neighbouring SMs (CG = 2)
 // computes 256 rows; each holds 128 rows of A and half of B's rows, and the
 // tensor cores of both read both halves of B. SUB = 2: a tile is two
 // accumulators of 256 columns that share A's slice, 256 x 512 in all: a slice
 // of 64 k costs an SM 48 KB for 1024 tensor cycles, 48 bytes per cycle (64 with
-// 256 x 256, 96 with one CTA's 128 x 256). CG = 1: one CTA, 128 x BN, for
-// products of few tiles.
+// 256 x 256, 96 with one CTA's 128 x 256). Products of few tiles take the kernel
+// of gemm_split.cuh, with single CTAs as well (CG = 1).
+//
+// Measured, 16384 x 4096 x 11264 with the power cap reached (the library's bf16
+// product alone: 1439 TFLOP/s of 8192^3, 1322 to 1390 of these shapes): gate 1291
+// TFLOP/s, down 1411, dx 1430, weight gradients 1418, the tensor pipe 88 to 95 %
+// busy; gradient of the gate 1029 (70 %), whose epilogue reads two and writes three
+// [M, F] tensors beside the products.
 //
 // Roles of a CTA's ten warps: 0 issues the copies into a ring of slices; 1
 // owns the tensor memory and issues the products (of the pair: the leader's);
@@ -92,10 +98,12 @@ struct Piece {
 };
 constexpr int gemm_piece_cols(int epi) { return epi == kEpiGateBwd ? 32 : 64; }
 
-template <int CG, int BN, int SUB, int EPI>
+constexpr int kPairN = 256;  // columns of an accumulator of the pair kernel
+
+template <int SUB, int EPI>
 struct GemmLayout {
   static constexpr int kA = kGemmM * 128;
-  static constexpr int kB = BN / CG * 128;
+  static constexpr int kB = kPairN / 2 * 128;
   static constexpr int kStage = kA + SUB * kB;
   static constexpr int kOutBytes = kGemmEpiWarps * kGemmOutBytes;
   static constexpr int kInBytes = EPI == kEpiGateBwd ? kGemmEpiWarps * 2 * Piece<32>::kBytes : 0;
@@ -105,7 +113,7 @@ struct GemmLayout {
   static constexpr int kIn = kOut + kOutBytes;
   static constexpr int kBars = kIn + kInBytes;
   static constexpr int kSmem = kBars + 512 + 1024;
-  static constexpr int kCols = 2 * BN;  // tensor memory columns
+  static constexpr int kCols = 2 * kPairN;  // tensor memory columns
   static_assert(kSmem <= kGemmMaxSmem && kStages >= 3, "shared memory");
   static_assert(kCols <= 512, "tensor memory");
 };
@@ -428,9 +436,10 @@ __device__ __forceinline__ void gemm_piece_bwd(const GemmArgs& P, const GemmProd
   if (P.save) ring.store(&Q.out[2], lane, row, col, [&](int, uint32_t* x) { copy16(w, x); });
 }
 
-template <int CG, int BN, int SUB, bool AMN, bool BMN, int EPI, int ACT>
+template <int SUB, bool AMN, bool BMN, int EPI, int ACT>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs P) {
-  using L = GemmLayout<CG, BN, SUB, EPI>;
+  using L = GemmLayout<SUB, EPI>;
+  constexpr int CG = 2, BN = kPairN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBars);  // slice landed (leader's: of both CTAs)
@@ -442,7 +451,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + kGemmEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
   int* status = P.status;
   if (threadIdx.x == 32) {
@@ -465,8 +474,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   }
   if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, L::kCols);
   tc_fence_before();
-  if constexpr (CG == 2) cluster_sync_all();
-  else __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   if (!P.beside) grid_dependency_wait();
@@ -489,20 +497,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
           const int seg = kc >= Q.slices0;
           const int k0 = (kc - (seg ? Q.slices0 : 0)) * kGemmK;
           uint32_t dst = smem_u32(sm + st * L::kStage);
-          uint32_t bar = smem_u32(&full[st]);
-          if constexpr (CG == 2) bar = map_shared(bar, 0);
+          const uint32_t bar = map_shared(smem_u32(&full[st]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[st], CG * (L::kA + U.subs * L::kB));
           gemm_load<CG, AMN>(dst, &Q.a[seg], bar, row0, k0, kGemmM);
           dst += L::kA;
           for (int i = 0; i < U.subs; ++i, dst += L::kB) {
             if constexpr (EPI == kEpiGate) {
               const int f0 = (U.sub + i) * (BN / 2);
-              if constexpr (CG == 2) {
-                gemm_load<CG, BMN>(dst, &Q.b[rank], bar, f0, k0, BN / 2);
-              } else {
-                gemm_load<CG, BMN>(dst, &Q.b[0], bar, f0, k0, BN / 2);
-                gemm_load<CG, BMN>(dst + BN / 2 * 128, &Q.b[1], bar, f0, k0, BN / 2);
-              }
+              gemm_load<CG, BMN>(dst, &Q.b[rank], bar, f0, k0, BN / 2);
             } else {
               gemm_load<CG, BMN>(dst, &Q.b[seg], bar, (U.sub + i) * BN + int(rank) * (BN / CG), k0, BN / CG);
             }
@@ -606,10 +608,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         auto release_acc = [&]() {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 2) mbar_arrive_cluster(map_shared(smem_u32(&acc_empty[acc]), 0));
-            else mbar_arrive(&acc_empty[acc]);
-          }
+          if (lane == 0) mbar_arrive_cluster(map_shared(smem_u32(&acc_empty[acc]), 0));
         };
         if constexpr (EPI == kEpiGateBwd) {
           auto fetch = [&](int c) {  // the saved projections of the piece at column c
@@ -654,23 +653,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   __syncwarp();
-  if (CG == 2 || EPI == kEpiGateBwd) {
-    // a CTA that gave up may leave copies of its own or of its pair on their way: let them land
-    if (*abort_flag) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 1000000) {
-      }
-      __syncwarp();
+  // a CTA that gave up may leave copies of its own or of its pair on their way: let them land
+  if (*abort_flag) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000) {
     }
+    __syncwarp();
   }
   tc_fence_before();
-  if constexpr (CG == 2) cluster_sync_all();
-  else __syncthreads();
+  cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_cg<CG>(tbase, L::kCols);
   }
-  if constexpr (CG == 2) cluster_sync_all();
+  cluster_sync_all();
   if (P.beside) grid_dependency_wait();
 }
 

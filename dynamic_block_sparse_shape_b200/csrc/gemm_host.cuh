@@ -55,9 +55,10 @@ inline void gemm_follow(const GemmArgs& P, cudaLaunchAttribute* at, int n, cudaL
   cfg->numAttrs = n;
 }
 
-template <int CG, int BN, int SUB, bool AMN, bool BMN, int EPI, int ACT>
+template <int SUB, bool AMN, bool BMN, int EPI, int ACT>
 prism_status gemm_launch(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s) {
-  using L = GemmLayout<CG, BN, SUB, EPI>;
+  using L = GemmLayout<SUB, EPI>;
+  constexpr int CG = 2, BN = kPairN;
   constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;
   constexpr int kRowsB = EPI == kEpiGate ? BN / 2 : BN / CG;
   P.products = products;
@@ -96,7 +97,7 @@ prism_status gemm_launch(GemmArgs& P, const GemmProblem* pr, int products, cudaS
   if (SUB == 2 && tiles % clusters * 2 <= clusters) P.whole = tiles / clusters * clusters;
   P.units = P.whole + 2 * (tiles - P.whole);
   if (clusters > P.units) clusters = P.units;
-  auto kernel = gemm_kernel<CG, BN, SUB, AMN, BMN, EPI, ACT>;
+  auto kernel = gemm_kernel<SUB, AMN, BMN, EPI, ACT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem) != cudaSuccess)
     return PRISM_ERR_CUDA;
   cudaLaunchConfig_t cfg;
@@ -262,7 +263,7 @@ prism_status gemm(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t
     ragged = ragged || pr[i].a[0].ld % 64 || pr[i].b[0].ld % 64;
   }
   const GemmChoice c = gemm_choice(m, n, products, slices, AMN, kSub, ragged, P.fine || P.fold);
-  if (c.bn == 0) return gemm_launch<2, 256, kSub, AMN, BMN, EPI, ACT>(P, pr, products, s);
+  if (c.bn == 0) return gemm_launch<kSub, AMN, BMN, EPI, ACT>(P, pr, products, s);
   if (c.cg == 1 && c.bn == 64) return gemm_split_launch<1, 64, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);
   if (c.cg == 1) return gemm_split_launch<1, 128, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);
   return gemm_split_launch<2, 256, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);
