@@ -7,8 +7,9 @@
 // its operands' bytes are spread over SMs. Splitting K needs the sums of the
 // parts: every CTA leaves its fp32 partial tile in its own shared memory (where
 // the operand slices were), and after a cluster barrier part r of the CTAs adds
-// column part r of all partial tiles in the order of the parts (the same bits
-// every time, no atomics, no workspace) and applies the epilogue. Of an operand
+// row part r of all partial tiles (whole rows: contiguous remote reads) in the
+// order of the parts (the same bits every time, no atomics, no workspace) and
+// applies the epilogue. Of an operand
 // A with fewer than 128 rows only those (rounded up to 8) are copied: the tensor
 // cores read stale rows beyond them, whose sums nobody reads.
 // A copy comes back after about 1.5 us, so the ring holds as many slices as
@@ -58,10 +59,16 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-// The sum over the parts, in their order, of 8 values at `at` (an address of
-// this CTA's partial tile): four parts' loads in flight at a time.
+// The sum over the parts, in their order, of 8 values at `at` of this CTA's
+// partial tile: four parts' loads in flight at a time.
 template <int CG>
-__device__ __forceinline__ void sum_parts(uint32_t at, int parts, uint32_t cta, float* v) {
+__device__ __forceinline__ void sum_parts(const float* part, int parts, uint32_t cta, float* v) {
+  if (parts == 1) {
+    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(part);
+    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(part + 4);
+    return;
+  }
+  const uint32_t at = smem_u32(part);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
   for (int p0 = 0; p0 < parts; p0 += 4) {
@@ -146,6 +153,29 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
     *abort_flag = 0;
     fence_barrier_init();
   }
+  auto copy = [&](int kc, int st) {
+    const int seg = kc >= Q.slices0;
+    const int k0 = (kc - (seg ? Q.slices0 : 0)) * kGemmK;
+    const uint32_t dst = smem_u32(sm + st * stage_bytes);
+    uint32_t bar = smem_u32(&full[st]);
+    if constexpr (CG == 2) bar = map_shared(bar, leader);
+    if (cta == 0) mbar_arrive_expect_tx(&full[st], CG * stage_bytes);
+    gemm_load<CG, AMN>(dst, &Q.a[seg], bar, row0, k0, kGemmM);
+    if constexpr (EPI == kEpiGate && CG == 2) {
+      gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[cta], bar, col0, k0, BN / 2);
+    } else if constexpr (EPI == kEpiGate) {
+      gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[0], bar, col0, k0, BN / 2);
+      gemm_load<CG, BMN>(dst + P.a_bytes + BN / 2 * 128, &Q.b[1], bar, col0, k0, BN / 2);
+    } else {
+      gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[seg], bar, col0 + int(cta) * (BN / CG), k0, BN / CG);
+    }
+  };
+  // a ring of fresh slices needs nothing of the others' setup (of a pair, the other CTA's barriers)
+  const int ahead = CG == 2 ? 0 : min(stages, last - first);
+  if (threadIdx.x == 0 && ahead > 0) {
+    if (!P.beside) grid_dependency_wait();
+    for (int i = 0; i < ahead; ++i) copy(first + i, i);
+  }
   if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, BN);
   tc_fence_before();
   if constexpr (CG == 2) cluster_sync_all();
@@ -159,26 +189,12 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      int st = 0, issued = 0;
-      uint32_t phase = 1;  // of `empty`: a fresh barrier passes
-      for (int kc = first; kc < last; ++kc, ++issued) {
+      int st = ahead == stages ? 0 : ahead, issued = ahead;
+      uint32_t phase = ahead == stages ? 0 : 1;  // of `empty`: a fresh barrier passes
+      for (int kc = first + ahead; kc < last; ++kc, ++issued) {
         ok = mbar_wait_abortable(&empty[st], phase, status, abort_flag);
         if (!ok) break;
-        const int seg = kc >= Q.slices0;
-        const int k0 = (kc - (seg ? Q.slices0 : 0)) * kGemmK;
-        const uint32_t dst = smem_u32(sm + st * stage_bytes);
-        uint32_t bar = smem_u32(&full[st]);
-        if constexpr (CG == 2) bar = map_shared(bar, leader);
-        if (cta == 0) mbar_arrive_expect_tx(&full[st], CG * stage_bytes);
-        gemm_load<CG, AMN>(dst, &Q.a[seg], bar, row0, k0, kGemmM);
-        if constexpr (EPI == kEpiGate && CG == 2) {
-          gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[cta], bar, col0, k0, BN / 2);
-        } else if constexpr (EPI == kEpiGate) {
-          gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[0], bar, col0, k0, BN / 2);
-          gemm_load<CG, BMN>(dst + P.a_bytes + BN / 2 * 128, &Q.b[1], bar, col0, k0, BN / 2);
-        } else {
-          gemm_load<CG, BMN>(dst + P.a_bytes, &Q.b[seg], bar, col0 + int(cta) * (BN / CG), k0, BN / CG);
-        }
+        copy(kc, st);
         if (++st == stages) {
           st = 0;
           phase ^= 1;
@@ -227,11 +243,23 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
       __syncwarp();
     }
   }
+  // the rows of the tile that this CTA finishes, 8 columns of a row per thread and step (n is a multiple of 8)
+  const int rows = min(kGemmM, Q.m - row0), vecs = (min(kCols, Q.n - col0) + 7) / 8;
+  const int rows_out = EPI == kEpiStore && P.fold ? P.fold : rows;
+  const int r0 = rows_out * part_of / parts, items = (rows_out * (part_of + 1) / parts - r0) * (kCols / 8);
+  uint4 gv = make_uint4(0, 0, 0, 0), uv = gv;
+  auto fetch = [&](int x) {  // the saved projections of step x
+    const int v = x % (kCols / 8);
+    if (x >= items || v >= vecs) return;
+    const int64_t at = int64_t(row0 + r0 + x / (kCols / 8)) * Q.n + col0 + 8 * v;
+    gv = __ldg(reinterpret_cast<const uint4*>(Q.in[0] + at));
+    uv = __ldg(reinterpret_cast<const uint4*>(Q.in[1] + at));
+  };
+  if constexpr (EPI == kEpiGateBwd) fetch(threadIdx.x);
   // every copy has landed and every product is complete: the slices' place is free
   __syncthreads();
   tc_fence_after();
   const bool gave_up = *abort_flag;
-  const int rows = min(kGemmM, Q.m - row0);
   float* part = reinterpret_cast<float*>(sm);
   if (warp >= 2) {
     const int q = warp & 3, half = (warp - 2) >> 2;
@@ -250,15 +278,13 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync_all();
-  // column part `part_of` of the tile: 8 columns of a row per thread and step
-  const int vecs = (min(kCols, Q.n - col0) + 7) / 8;  // n is a multiple of 8
-  const int v0 = vecs * part_of / parts, mine = vecs * (part_of + 1) / parts - v0;
-  if (!gave_up && mine > 0) {
-    const int out_rows = EPI == kEpiStore && P.fold ? P.fold : rows;
-    for (int x = threadIdx.x; x < out_rows * mine; x += kGemmThreads) {
-      const int r = x / mine, v = v0 + x - r * mine;
-      const uint32_t at = smem_u32(part + r * kPitch + 8 * v);
+  if (ranks == 1) __syncthreads();
+  else cluster_sync_all();
+  if (!gave_up) {
+    for (int x = threadIdx.x; x < items; x += kGemmThreads) {
+      const int r = r0 + x / (kCols / 8), v = x % (kCols / 8);
+      if (v >= vecs) continue;
+      const float* at = part + r * kPitch + 8 * v;
       const int64_t row = row0 + r;
       const int col = col0 + 8 * v;
       float d[8];
@@ -266,14 +292,14 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
       if constexpr (EPI == kEpiStore) {
         if (P.fold) {
           float e[8];
-          sum_parts<CG>(at + P.fold * kPitch * 4, parts, cta, e);
+          sum_parts<CG>(at + P.fold * kPitch, parts, cta, e);
 #pragma unroll
           for (int i = 0; i < 8; ++i) d[i] += e[i];
         }
         *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(d);
       } else if constexpr (EPI == kEpiGate) {
         float u[8], h[8];
-        sum_parts<CG>(at + BN / 2 * 4, parts, cta, u);
+        sum_parts<CG>(at + BN / 2, parts, cta, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = act_f<ACT>(d[i]) * u[i];
         store8(Q.out[0] + row * Q.out_ld[0] + col, h, P.fine, Q.m * Q.out_ld[0]);
@@ -283,8 +309,9 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
         }
       } else {
         float g[8], u[8], dg[8], du[8], h[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(Q.in[0] + row * Q.n + col)), g);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(Q.in[1] + row * Q.n + col)), u);
+        unpack8(gv, g);
+        unpack8(uv, u);
+        fetch(x + kGemmThreads);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float a, s;
@@ -300,7 +327,8 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
     }
   }
   __syncwarp();
-  cluster_sync_all();  // nobody reads this CTA's partial tile any more
+  if (ranks == 1) __syncthreads();
+  else cluster_sync_all();  // nobody reads this CTA's partial tile any more
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_cg<CG>(tbase, BN);
