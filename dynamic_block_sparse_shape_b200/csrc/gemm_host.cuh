@@ -124,6 +124,12 @@ inline int64_t split_slots(int ranks, int per_sm) {
   return int64_t(device_sm_count()) * per_sm - idle;
 }
 
+constexpr int kSplitHalf = 113 * 1024;  // shared memory of each of two CTAs on an SM
+
+inline int split_slot_rows(int a_rows, int fold, int parts) {
+  return fold ? 2 * ((fold + parts - 1) / parts) : (a_rows + parts - 1) / parts;
+}
+
 template <int CG, int BN, bool AMN, bool BMN, int EPI, int ACT>
 prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int products, int parts, cudaStream_t s) {
   constexpr int kCols = EPI == kEpiGate ? BN / 2 : BN;
@@ -166,10 +172,13 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
   const int ranks = CG * parts;
   if (tiles * ranks >= (int64_t(1) << 31)) return PRISM_ERR_UNSUPPORTED;
   // a ring of all of an SM's shared memory, or two of half of it
-  const int room = CG == 2 || tiles * ranks <= split_slots(ranks, 1) ? kGemmMaxSmem : 113 * 1024;
+  A.slot_rows = split_slot_rows(a_rows, P.fold, parts);
+  const auto need = [&](int stages) { return split_smem(CG, BN, A.a_bytes, stages, parts, A.slot_rows); };
+  const int room = CG == 2 || tiles * ranks <= split_slots(ranks, 1) || need(1) > kSplitHalf ? kGemmMaxSmem : kSplitHalf;
   A.stages = int(std::min<int64_t>(kSplitStages, (slices + parts - 1) / parts));
-  while (A.stages > 1 && split_smem(CG, BN, A.a_bytes, A.stages) > room) --A.stages;
-  const int smem = split_smem(CG, BN, A.a_bytes, A.stages);
+  while (A.stages > 1 && need(A.stages) > room) --A.stages;
+  const int smem = need(A.stages);
+  if (smem > room) return PRISM_ERR_UNSUPPORTED;  // see gemm_choice
   auto kernel = gemm_split_kernel<CG, BN, AMN, BMN, EPI, ACT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmMaxSmem) != cudaSuccess)
     return PRISM_ERR_CUDA;
@@ -227,10 +236,12 @@ inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, 
     const int rows_a = a_mn || t.cg == 2 || m[0] >= kGemmM ? kGemmM : int(m[0] + 7) / 8 * 8;
     const double bytes = (rows_a + t.bn / t.cg) * 128.0;
     for (int parts = 1; parts <= t.parts && parts <= slices; parts *= 2) {
+      const int least = split_smem(t.cg, t.bn, rows_a * 128, 1, parts, split_slot_rows(rows_a, 0, parts) + 1);
+      if (least > kGemmMaxSmem) continue;
       const int64_t ctas = int64_t(tiles(kGemmM * t.cg, t.bn)) * t.cg * parts, one_each = split_slots(t.cg * parts, 1);
       // rounds of CTAs, and how many an SM works through in all
       int64_t rounds = (ctas + one_each - 1) / one_each, load = rounds;
-      if (t.cg == 1 && rounds > 1) {
+      if (t.cg == 1 && rounds > 1 && least <= kSplitHalf) {
         const int64_t two_each = split_slots(parts, 2);
         rounds = (ctas + two_each - 1) / two_each;
         load = 2 * rounds - (ctas - (rounds - 1) * two_each <= one_each);

@@ -6,9 +6,10 @@
 // fetches at most some 90 GB/s from L2 (measured), so a product is as fast as
 // its operands' bytes are spread over SMs. Splitting K needs the sums of the
 // parts: every CTA leaves its fp32 partial tile in its own shared memory (where
-// the operand slices were), and after a cluster barrier part r of the CTAs adds
-// row part r of all partial tiles (whole rows: contiguous remote reads) in the
-// order of the parts (the same bits every time, no atomics, no workspace) and
+// the operand slices were), and after a cluster barrier sends row part r of it to
+// part r of the CTAs in one bulk copy (loads of the other CTAs' shared memory
+// took 3 to 4 us for the same, 128 x 128 in 4 parts); that one adds what it got in
+// the order of the parts (the same bits every time, no atomics, no workspace) and
 // applies the epilogue. Of an operand
 // A with fewer than 128 rows only those (rounded up to 8) are copied: the tensor
 // cores read stale rows beyond them, whose sums nobody reads.
@@ -37,55 +38,42 @@ struct SplitLaunch {
   SplitArgs p[kGemmProducts];
   int products, save, beside, fine, fold;  // see GemmArgs
   int a_bytes, stages;  // of A's part of a slice, and slices of the ring
+  int slot_rows;        // rows of a part's share of another CTA's rows, at most
   int* status;
 };
 
 // Shared memory: barriers (1 KB), then the ring. The tensor cores read 16 KB
 // from the start of a slice's A, whatever was copied, so the last slice is
-// followed by room for that. The fp32 partial tile takes the ring's place.
+// followed by room for that. The fp32 partial tile and what the other parts send
+// take the ring's place.
 constexpr int kSplitBars = 1024;
 constexpr int split_pitch(int bn) { return bn + 4; }  // floats between its rows: 16 bytes modulo 32 banks apart
-constexpr int split_smem(int cg, int bn, int a_bytes, int stages) {
+constexpr int split_tile_rows(int a_bytes) { return (a_bytes / 128 + 31) / 32 * 32; }  // a warp's 32 rows at a time
+constexpr int split_smem(int cg, int bn, int a_bytes, int stages, int parts, int slot_rows) {
   const int ring = stages * (a_bytes + bn / cg * 128) + kGemmM * 128 - a_bytes;
-  const int tile = (a_bytes / 128 + 31) / 32 * 32 * split_pitch(bn) * 4;  // a warp's 32 rows at a time
+  const int tile = (split_tile_rows(a_bytes) + (parts - 1) * slot_rows) * split_pitch(bn) * 4;
   return 1024 + kSplitBars + (ring > tile ? ring : tile);
 }
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
+// `bytes` (a multiple of 16) of this CTA's shared memory to another of its
+// cluster, counted on that one's barrier.
+__device__ __forceinline__ void bulk_send(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
-// The sum over the parts, in their order, of 8 values at `at` of this CTA's
-// partial tile: four parts' loads in flight at a time.
-template <int CG>
-__device__ __forceinline__ void sum_parts(const float* part, int parts, uint32_t cta, float* v) {
-  if (parts == 1) {
-    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(part);
-    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(part + 4);
-    return;
-  }
-  const uint32_t at = smem_u32(part);
+// The sum over the parts, in their order, of 8 values: this CTA's at `own`, part
+// p's at `got` + (p or, behind this CTA's, p - 1) * slot.
+__device__ __forceinline__ void sum_parts(const float* own, const float* got, int slot, int parts, int part_of, float* v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  for (int p0 = 0; p0 < parts; p0 += 4) {
-    float4 x[4], y[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-      if (p0 + p < parts) {
-        const uint32_t a = map_shared(at, CG * (p0 + p) + cta);
-        x[p] = ld_cluster_f4(a);
-        y[p] = ld_cluster_f4(a + 16);
-      }
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-      if (p0 + p < parts) {
-        v[0] += x[p].x; v[1] += x[p].y; v[2] += x[p].z; v[3] += x[p].w;
-        v[4] += y[p].x; v[5] += y[p].y; v[6] += y[p].z; v[7] += y[p].w;
-      }
+  for (int p = 0; p < parts; ++p) {
+    const float* a = p == part_of ? own : got;
+    if (p != part_of) got += slot;
+    const float4 x = *reinterpret_cast<const float4*>(a), y = *reinterpret_cast<const float4*>(a + 4);
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
   }
 }
 
@@ -122,7 +110,8 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
   uint64_t* full = reinterpret_cast<uint64_t*>(sm);
   uint64_t* empty = full + kSplitStages;
   uint64_t* acc_full = empty + kSplitStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint64_t* joined = acc_full + 1;  // the other parts' rows have come
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank(), cta = CG == 2 ? rank & 1 : 0, leader = rank - cta;
@@ -150,6 +139,7 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
       mbar_init(&empty[i], 1);
     }
     mbar_init(acc_full, 1);
+    mbar_init(joined, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -246,7 +236,8 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
   // the rows of the tile that this CTA finishes, 8 columns of a row per thread and step (n is a multiple of 8)
   const int rows = min(kGemmM, Q.m - row0), vecs = (min(kCols, Q.n - col0) + 7) / 8;
   const int rows_out = EPI == kEpiStore && P.fold ? P.fold : rows;
-  const int r0 = rows_out * part_of / parts, items = (rows_out * (part_of + 1) / parts - r0) * (kCols / 8);
+  auto row_part = [&](int p) { return rows_out * p / parts; };
+  const int r0 = row_part(part_of), mine = row_part(part_of + 1) - r0, items = mine * (kCols / 8);
   uint4 gv = make_uint4(0, 0, 0, 0), uv = gv;
   auto fetch = [&](int x) {  // the saved projections of step x
     const int v = x % (kCols / 8);
@@ -261,6 +252,7 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
   tc_fence_after();
   const bool gave_up = *abort_flag;
   float* part = reinterpret_cast<float*>(sm);
+  float* got = part + split_tile_rows(P.a_bytes) * kPitch;
   if (warp >= 2) {
     const int q = warp & 3, half = (warp - 2) >> 2;
     if (32 * q < rows) {
@@ -276,30 +268,46 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
       }
     }
   }
+  if (parts > 1) fence_proxy_async_smem();
   __syncwarp();
   tc_fence_before();
   if (ranks == 1) __syncthreads();
   else cluster_sync_all();
+  if (parts > 1) {
+    const int folds = EPI == kEpiStore && P.fold ? 2 : 1;  // runs of rows that a part sends to another
+    if (threadIdx.x == 0 && mine > 0) mbar_arrive_expect_tx(joined, (parts - 1) * folds * mine * kPitch * 4);
+    if (warp == 0 && lane < parts && lane != part_of) {
+      const int to0 = row_part(lane), n = row_part(lane + 1) - to0;
+      const uint32_t to = CG * lane + cta, bar = map_shared(smem_u32(joined), to);
+      const uint32_t dst = map_shared(smem_u32(got + (part_of - (part_of > lane)) * P.slot_rows * kPitch), to);
+      if (n > 0) {
+        for (int i = 0; i < folds; ++i)
+          bulk_send(dst + i * n * kPitch * 4, part + (to0 + i * P.fold) * kPitch, n * kPitch * 4, bar);
+      }
+    }
+    if (mine > 0) mbar_wait(joined, 0, status);
+  }
   if (!gave_up) {
     for (int x = threadIdx.x; x < items; x += kGemmThreads) {
       const int r = r0 + x / (kCols / 8), v = x % (kCols / 8);
       if (v >= vecs) continue;
-      const float* at = part + r * kPitch + 8 * v;
+      const float *own = part + r * kPitch + 8 * v, *sent = got + (r - r0) * kPitch + 8 * v;
+      const int slot = P.slot_rows * kPitch;
       const int64_t row = row0 + r;
       const int col = col0 + 8 * v;
       float d[8];
-      sum_parts<CG>(at, parts, cta, d);
+      sum_parts(own, sent, slot, parts, part_of, d);
       if constexpr (EPI == kEpiStore) {
         if (P.fold) {
           float e[8];
-          sum_parts<CG>(at + P.fold * kPitch, parts, cta, e);
+          sum_parts(own + P.fold * kPitch, sent + mine * kPitch, slot, parts, part_of, e);
 #pragma unroll
           for (int i = 0; i < 8; ++i) d[i] += e[i];
         }
         *reinterpret_cast<uint4*>(Q.out[0] + row * Q.out_ld[0] + col) = pack8(d);
       } else if constexpr (EPI == kEpiGate) {
         float u[8], h[8];
-        sum_parts<CG>(at + BN / 2, parts, cta, u);
+        sum_parts(own + BN / 2, sent + BN / 2, slot, parts, part_of, u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = act_f<ACT>(d[i]) * u[i];
         store8(Q.out[0] + row * Q.out_ld[0] + col, h, P.fine, Q.m * Q.out_ld[0]);
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(kGemmThreads, CG == 2 ? 1 : 2) gemm_split_kern
   }
   __syncwarp();
   if (ranks == 1) __syncthreads();
-  else cluster_sync_all();  // nobody reads this CTA's partial tile any more
+  else cluster_sync_all();  // all that this CTA sent has come
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_cg<CG>(tbase, BN);
