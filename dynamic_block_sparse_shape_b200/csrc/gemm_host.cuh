@@ -197,13 +197,15 @@ prism_status gemm_split_launch(const GemmArgs& P, const GemmProblem* pr, int pro
   return cuda_status(cudaLaunchKernelEx(&cfg, kernel, A));
 }
 
-// Time of a product in ns by what it is made of (measured on products of 16 to
-// 2000 rows): an SM fetches kRate bytes per ns from L2, rows that do not start
-// on 128-byte borders count kRagged times; a slice takes at least its tensor
-// cycles and kSliceNs, and a ring's slices come back after kLatencyNs; a tile's
-// fill and epilogue, and the joining of parts.
-constexpr double kRate = 90.0, kRagged = 1.3, kLatencyNs = 1500.0, kSliceNs = 250.0, kCycleNs = 1.0 / 1.7,
-                 kTileNs = 6000.0, kJoinNs = 1500.0, kJoinRate = 60.0;
+// Time of a product in ns by what it is made of (fitted to the measured times of
+// ten choices each for the products of 13 sizes of 33 to 3000 rows; the choices it
+// takes are 0.9 % behind the best ones in the mean, 14 % at worst): an SM fetches
+// kRate bytes per ns from L2, rows that do not start on 128-byte borders count
+// kRagged times; a slice takes at least its tensor cycles and a CTA kSliceNs, and
+// a ring's slices come back after kLatencyNs; a tile's fill and epilogue, of a
+// single CTA, a pair, and the persistent pairs; and the joining of parts.
+constexpr double kRate = 90.0, kRagged = 1.3, kLatencyNs = 1200.0, kSliceNs = 350.0, kCycleNs = 1.0 / 1.7,
+                 kTileNs = 4500.0, kPairTileNs = 6000.0, kPersistentNs = 5000.0, kJoinNs = 300.0, kJoinRate = 40.0;
 
 struct GemmChoice {
   int cg, bn, parts;  // bn = 0: the pair kernel of gemm.cuh
@@ -227,7 +229,7 @@ inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, 
   const double whole = std::floor(accs / sub / pairs), rest = accs / sub - whole * pairs;
   const double one = std::fmax(32768.0 / rate, 512 * kCycleNs);
   const double both = sub == 1 ? one : std::fmax(49152.0 / rate, 1024 * kCycleNs);
-  double best = k * (whole * both + (rest > 0 ? (rest * 2 <= pairs ? one : both) : 0.0)) + kTileNs;
+  double best = k * (whole * both + (rest > 0 ? (rest * 2 <= pairs ? one : both) : 0.0)) + kPersistentNs;
   GemmChoice c = {2, 0, 1};
   if (single) best = HUGE_VAL;
   const GemmChoice tries[] = {{1, 64, 8}, {1, 128, 4}, {2, 256, 4}};  // with the most parts
@@ -249,9 +251,9 @@ inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, 
       const double mine = std::ceil(k / parts);
       const double flight = std::fmin(std::fmin(mine, double(kSplitStages)) * (t.cg == 1 && load > 1 ? 2.0 : 1.0),
                                       kGemmMaxSmem / bytes);
-      const double slice = std::fmax(std::fmax(bytes / rate, kSliceNs), kLatencyNs / std::fmax(flight, 1.0));
+      const double slice = std::fmax(std::fmax(bytes / rate, load > rounds ? kSliceNs / 2 : kSliceNs), kLatencyNs / std::fmax(flight, 1.0));
       const double join = parts > 1 ? double(rounds) * kJoinNs + double(load) * rows_a * t.bn * 4.0 / kJoinRate : 0.0;
-      const double ns = double(load) * mine * slice + double(rounds) * kTileNs + join;
+      const double ns = double(load) * mine * slice + double(rounds) * (t.cg == 2 ? kPairTileNs : kTileNs) + join;
       if (ns < best) {
         best = ns;
         c = {t.cg, t.bn, parts};
