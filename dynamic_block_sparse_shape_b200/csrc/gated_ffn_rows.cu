@@ -15,7 +15,7 @@
 // bf16 values and m rows of their bf16 remainders; the down product takes them as
 // 2 m tokens and adds the two, so y is rounded once and not on top of a rounded h.
 // 2048 x 5632, cold weights: 1 and 4 tokens 18.3 us, 8 tokens 20.8, 16 24.0 in both
-// launches (the tiles of the split kernel: 29 to 31; multiply-adds on the ordinary
+// launches (the tiles of the split kernel: 25 to 26; multiply-adds on the ordinary
 // cores: 18.8 for one token, 45 for 8). h rounded to bf16 instead: 18.2 for one
 // token, 19.0 for 8, 23.2 for 16, with 1.41 times the error of y; h in fp32, split
 // as it is read: 20.3 and 29.4 for 1 and 16.
@@ -181,9 +181,9 @@ prism_status rows_for(const RowArgs& a, bool follows, cudaStream_t s) {
 
 // Up to 8 tokens, and up to 16 where a CTA per SM at most takes the down product:
 // each reads all of h, by then more than its weights. 16 tokens, this way / by
-// tiles: 2048 x 5632 24.0 / 30.8 us, 2368 x 6400 29.0 / 33.2, 2384 x 6400 49.4 /
-// 34.2, 4096 x 11264 104 / 61.6; 8 tokens: 4096 x 11264 50 / 60, 8192 x 22528
-// 185 / 209.
+// tiles: 1024 x 2816 13.3 / 15.5 us, 2048 x 5632 24.2 / 24.8, 2368 x 6400 28.9 /
+// 29.3, 2384 x 6400 49.4 / 29.8, 4096 x 11264 104 / 63; 8 tokens: 2048 x 5632 20.7
+// / 25.8, 4096 x 11264 52 / 63, 8192 x 22528 186 / 198.
 bool ffn_takes_rows(int64_t m, int d) { return m <= 8 || (m <= 16 && (d + kRowTile - 1) / kRowTile <= device_sm_count()); }
 
 prism_status ffn_rows_forward(int act, const prism_ffn_weights& w, int m, const void* x, int64_t x_ld, void* h, void* y,
