@@ -8,6 +8,7 @@ calling an entry point without the built library raises ``PrismError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -616,6 +617,8 @@ _ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 def _row_stride(t: torch.Tensor, rows, cols, what: str, name: str) -> int:
     """Elements between the rows of a [rows, cols] matrix with contiguous rows."""
+    if t.is_contiguous() and t.shape == (rows, cols) and cols % 8 == 0:
+        return cols
     if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
         _require(False, f"{what}: {name} must be [{rows}, {cols}]")
     s0, s1 = t.stride()
@@ -633,10 +636,20 @@ def _ffn_weights(w_gate, w_up, w_down, what):
                        _row_stride(w_down, d, f, what, "w_down"), d, f), d, f
 
 
-def _ffn_workspace(ws, m, f, backward, device):
+@functools.lru_cache(maxsize=256)
+def _ffn_workspace_bytes(m, f, backward):
     b = _SZ()
     _check(lib().prism_gated_ffn_workspace_size(m, f, backward, ctypes.byref(b)), "prism_gated_ffn_workspace_size")
-    return (ws or Workspace(device, b.value)).ensure(b.value)
+    return b.value
+
+
+def _ffn_workspace(ws, m, f, backward, device):
+    """The workspace, and its aligned start and the bytes from there."""
+    need = _ffn_workspace_bytes(m, f, backward)
+    buf = (ws or Workspace(device, need)).ensure(need).buf
+    p = buf.data_ptr()
+    start = (p + 255) // 256 * 256
+    return buf, start, buf.numel() - (start - p)
 
 
 def _new_like(t: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
@@ -667,7 +680,7 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
     m = x.shape[0] if x.dim() else 0
     sx = _row_stride(x, m, d, what, "x")
     with _On(every, stream, what) as on:
-        ws = _ffn_workspace(ws, m, f, 0, x.device)
+        buf, start, nbytes = _ffn_workspace(ws, m, f, 0, x.device)
         y, gate, up, gp, upp = out, None, None, None, None
         if out is None:
             y = _new_like(x, m, d)
@@ -678,9 +691,9 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
             gate = x.new_empty(m, f)
             up = x.new_empty(m, f)
             gp, upp = gate.data_ptr(), up.data_ptr()
-        on.made(y, gate, up, ws.buf)
+        on.made(y, gate, up, buf)
         _check(lib().prism_gated_ffn_fwd(ctypes.byref(w), m, _ACT[act], code, x.data_ptr(), sx, y.data_ptr(), sy, gp, upp,
-                                         ws.ptr, ws.nbytes, on.ptr), what)
+                                         start, nbytes, on.ptr), what)
     return y, gate, up
 
 
@@ -701,7 +714,7 @@ def gated_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up:
         if t.shape != (m, f) or not t.is_contiguous():
             _require(False, what + ": gate and up must be contiguous [m, f]")
     with _On(every, stream, what) as on:
-        ws = _ffn_workspace(ws, m, f, 1, x.device)
+        buf, start, nbytes = _ffn_workspace(ws, m, f, 1, x.device)
         dx = dwg = dwu = dwd = xp = gp = upp = dp = None
         if need_dx:
             dx = _new_like(x, m, d)
@@ -709,10 +722,9 @@ def gated_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up:
         if need_dw:
             dwg, dwu, dwd = _new_like(w_gate, f, d), _new_like(w_up, f, d), _new_like(w_down, d, f)
             gp, upp, dp = dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()
-        on.made(dx, dwg, dwu, dwd, ws.buf)
+        on.made(dx, dwg, dwu, dwd, buf)
         _check(lib().prism_gated_ffn_bwd(ctypes.byref(w), m, _ACT[act], code, dy.data_ptr(), sdy, x.data_ptr(), sx,
-                                         gate.data_ptr(), up.data_ptr(), xp, d, gp, upp, dp, ws.ptr, ws.nbytes, on.ptr),
-               what)
+                                         gate.data_ptr(), up.data_ptr(), xp, d, gp, upp, dp, start, nbytes, on.ptr), what)
     return dx, dwg, dwu, dwd
 
 
