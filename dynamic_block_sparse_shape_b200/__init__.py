@@ -219,8 +219,11 @@ def workspace_size(op: str, geo: Geometry, heads=1, head_dim=128, feat_c=0, res_
 
 class Workspace:
     """A caller-owned device scratch buffer (torch allocation, 256-byte aligned)
-    that grows on demand. The library itself never allocates. A buffer that a
-    captured graph may hold stays allocated when a larger one takes its place."""
+    that grows on demand. The library itself never allocates. It belongs to the
+    stream that is current when it is made or grows; calls on other streams are
+    noted, so its memory is not handed on before they are done. Calls that share
+    a workspace must be ordered one behind the other. A buffer that a captured
+    graph may hold stays allocated when a larger one takes its place."""
 
     def __init__(self, device="cuda", nbytes=1 << 20):
         self.device = torch.device(device)
@@ -230,43 +233,111 @@ class Workspace:
         self.ensure(nbytes)
 
     def ensure(self, nbytes: int):
+        """Makes room for `nbytes`, for work on the current stream."""
         nbytes = max(int(nbytes), 256)
-        if self.buf is None or self.buf.numel() < nbytes:
+        if self.device.index is not None and self.device.index != torch._C._cuda_getDevice():
+            with torch.cuda.device(self.device):
+                return self._ensure(nbytes)
+        return self._ensure(nbytes)
+
+    def _ensure(self, nbytes: int):
+        if self.buf is None or self.buf.numel() < nbytes + 256:
             if self.captured:
                 self.kept.append(self.buf)
-            self.buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
+            self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
+            self.start = (self.buf.data_ptr() + 255) // 256 * 256
+            at = self.start - self.buf.data_ptr()
+            self.buf[at:at + 256].zero_()  # the status word: every call writes the rest before it reads it
             self.captured = False
-        if self.buf.is_cuda and torch.cuda.is_current_stream_capturing():
-            self.captured = True
+            self.device = self.buf.device
+            self.home = _raw_stream(self.device.index) if self.buf.is_cuda else None
+        if self.buf.is_cuda:
+            if _raw_stream(self.device.index) != self.home:
+                self.buf.record_stream(torch.cuda.current_stream(self.device))
+            if torch.cuda.is_current_stream_capturing():
+                self.captured = True
         return self
 
     @property
     def ptr(self):
-        p = self.buf.data_ptr()
-        return ctypes.c_void_p((p + 255) // 256 * 256)
+        return ctypes.c_void_p(self.start)
 
     @property
     def nbytes(self):
-        p = self.buf.data_ptr()
-        return self.buf.numel() - ((p + 255) // 256 * 256 - p)
+        return self.buf.numel() - (self.start - self.buf.data_ptr())
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _require(ok: bool, what: str, status: int = 1):
+    if not ok:
+        raise PrismError(status, what)
+
+
+class _On:
+    """The device and the stream of a call made current: those of its tensors (of the current device without any), and
+    the stream given or that device's current one (`ptr`). What the call allocates then belongs to its stream; results
+    are noted on the caller's stream as well (`made`), which goes on to read them."""
+    __slots__ = ("guard", "caller", "ptr", "device")
+
+    def __init__(self, tensors, stream, what):
+        index = tensors[0].get_device() if tensors else torch.cuda.current_device()
+        for t in tensors:
+            if t.get_device() != index:
+                _require(False, what + ": tensors on different devices")
+        if index < 0:
+            _require(False, what + ": tensors must be on a CUDA device")
+        self.device = index
+        self.guard = self.caller = None
+        self.ptr = _raw_stream(index)
+        if stream is not None and stream.cuda_stream != self.ptr:
+            _require(stream.device_index == index, what + ": a stream of another device")
+            self.caller = torch.cuda.current_stream(index)
+            self.ptr = stream.cuda_stream
+            self.guard = torch.cuda.stream(stream)
+        elif index != torch._C._cuda_getDevice():
+            self.guard = torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def made(self, *tensors):
+        if self.caller is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.caller)
+
+    def workspace(self, ws: Optional[Workspace], nbytes: int, what: str) -> Workspace:
+        """The workspace given, or one for this call, with room for `nbytes`."""
+        if ws is None:
+            return Workspace(torch.device("cuda", self.device), nbytes)
+        if ws.buf.get_device() != self.device:
+            _require(False, what + ": a workspace of another device", 4)
+        return ws.ensure(nbytes)
 
 
 def check_device_status(ws: Workspace, stream=None):
-    _check(lib().prism_check_device_status(ws.ptr, _stream(stream)), "device status")
+    with _On([ws.buf], stream, "device status") as on:
+        _check(lib().prism_check_device_status(ws.ptr, on.ptr), "device status")
 
 
 def zone_shapes(geo: Geometry, feat: Optional[torch.Tensor] = None, res: Optional[torch.Tensor] = None,
                 params: Optional[ShapeParams] = None, ws: Optional[Workspace] = None, stream=None):
     """a1+a2: per-zone candidate index (int32 [n_zones]) and cost margin (fp32)."""
+    what = "prism_zone_shapes"
     nz, _ = geo.counts()
-    device = (feat if feat is not None else res).device if (feat is not None or res is not None) else "cuda"
     feat_c = feat.shape[1] if feat is not None else 0
     res_c = res.shape[1] if res is not None else 0
     fdt = feat.dtype if feat is not None else torch.bfloat16
     need = workspace_size("zone_shapes", geo, feat_c=feat_c, res_c=res_c, dtype=fdt)
-    ws = (ws or Workspace(device)).ensure(need)
-    shape = torch.empty(nz, dtype=torch.int32, device=device)
-    margin = torch.empty(nz, dtype=torch.float32, device=device)
     p = params or ShapeParams()
     cp = _ShapeParams(p.w_audio, p.gamma, p.gate_max)
     g = geo.c()
@@ -274,11 +345,17 @@ def zone_shapes(geo: Geometry, feat: Optional[torch.Tensor] = None, res: Optiona
         assert feat.stride(1) == 1
     if res is not None:
         assert res.stride(1) == 1
-    _check(lib().prism_zone_shapes(
-        ctypes.byref(g), _ptr(feat), feat.stride(0) if feat is not None else 0, feat_c,
-        _dtype_code(feat) if feat is not None else BF16, _ptr(res), res.stride(0) if res is not None else 0, res_c,
-        _dtype_code(res) if res is not None else BF16, ctypes.byref(cp), _ptr(shape), _ptr(margin), ws.ptr, ws.nbytes,
-        _stream(stream)), "prism_zone_shapes")
+    tensors = [t for t in (feat, res) if t is not None] or ([ws.buf] if ws is not None else [])
+    with _On(tensors, stream, what) as on:
+        ws = on.workspace(ws, need, what)
+        shape = torch.empty(nz, dtype=torch.int32, device=ws.device)
+        margin = torch.empty(nz, dtype=torch.float32, device=ws.device)
+        on.made(shape, margin)
+        _check(lib().prism_zone_shapes(
+            ctypes.byref(g), _ptr(feat), feat.stride(0) if feat is not None else 0, feat_c,
+            _dtype_code(feat) if feat is not None else BF16, _ptr(res), res.stride(0) if res is not None else 0, res_c,
+            _dtype_code(res) if res is not None else BF16, ctypes.byref(cp), _ptr(shape), _ptr(margin), ws.ptr,
+            ws.nbytes, on.ptr), what)
     return shape, margin
 
 
@@ -288,13 +365,15 @@ def block_pool(geo: Geometry, zone_shape: torch.Tensor, q: torch.Tensor, k: torc
     _, nb = geo.counts()
     N, H, d = q.shape
     assert q.stride(2) == 1 and q.stride(1) == d and k.stride() == q.stride()
-    ws = (ws or Workspace(q.device)).ensure(256)
-    qp = torch.empty((H, nb, d), dtype=torch.float32, device=q.device)
-    kp = torch.empty_like(qp)
+    what = "prism_block_pool"
     g = geo.c()
-    _check(lib().prism_block_pool(ctypes.byref(g), _ptr(zone_shape), _ptr(q), _ptr(k), _dtype_code(q), H, d,
-                                  q.stride(0), _ptr(qp), _ptr(kp), ws.ptr, ws.nbytes, _stream(stream)),
-           "prism_block_pool")
+    with _On((zone_shape, q, k), stream, what) as on:
+        ws = on.workspace(ws, 256, what)
+        qp = torch.empty((H, nb, d), dtype=torch.float32, device=q.device)
+        kp = torch.empty_like(qp)
+        on.made(qp, kp)
+        _check(lib().prism_block_pool(ctypes.byref(g), _ptr(zone_shape), _ptr(q), _ptr(k), _dtype_code(q), H, d,
+                                      q.stride(0), _ptr(qp), _ptr(kp), ws.ptr, ws.nbytes, on.ptr), what)
     return qp, kp
 
 
@@ -306,6 +385,28 @@ def select_workspace_size(heads: int, n_blocks: int, head_dim: int) -> int:
     return int(b.value)
 
 
+def _select(call, tensors, ws, csr, stream, what):
+    """Outputs of a selection over the pooled tensors; `call` runs it."""
+    H, nb, d = tensors[0].shape
+    words = (nb + 31) // 32
+    dev = tensors[0].device
+    with _On(tensors, stream, what) as on:
+        ws = on.workspace(ws, select_workspace_size(H, nb, d), what)
+        mask = torch.empty((H, nb, words), dtype=torch.int32, device=dev)
+        kept = torch.empty((H, nb), dtype=torch.int32, device=dev)
+        row_ptr = torch.empty(H * nb + 1, dtype=torch.int32, device=dev)
+        on.made(mask, kept, row_ptr)
+        total = _I64()
+        _check(call(ws, mask, kept, row_ptr, total, on.ptr), what)
+        out = {"mask": mask, "kept": kept, "row_ptr": row_ptr, "total": int(total.value), "col_idx": None}
+        if csr:
+            col = torch.empty(max(1, total.value), dtype=torch.int32, device=dev)
+            on.made(col)
+            mask_to_csr(mask, row_ptr, nb, col, ws=ws)
+            out["col_idx"] = col[:total.value]
+    return out
+
+
 def block_select(qp: torch.Tensor, kp: torch.Tensor, scale: float, top_k: int,
                  cdf_threshold: float = DEFAULT_CDF_THRESHOLD, ws: Optional[Workspace] = None, csr: bool = True,
                  stream=None):
@@ -313,22 +414,13 @@ def block_select(qp: torch.Tensor, kp: torch.Tensor, scale: float, top_k: int,
     the uint32 words [H, nb, ceil(nb/32)]), kept [H, nb], row_ptr [H*nb+1],
     col_idx [total] and total (int)."""
     H, nb, d = qp.shape
-    words = (nb + 31) // 32
-    dev = qp.device
-    ws = (ws or Workspace(dev)).ensure(select_workspace_size(H, nb, d))
-    mask = torch.empty((H, nb, words), dtype=torch.int32, device=dev)
-    kept = torch.empty((H, nb), dtype=torch.int32, device=dev)
-    row_ptr = torch.empty(H * nb + 1, dtype=torch.int32, device=dev)
-    total = _I64()
-    _check(lib().prism_block_select(_ptr(qp), _ptr(kp), H, nb, d, float(scale), int(top_k), float(cdf_threshold),
-                                    _ptr(mask), _ptr(kept), _ptr(row_ptr), None, 0, ctypes.byref(total), ws.ptr,
-                                    ws.nbytes, _stream(stream)), "prism_block_select")
-    out = {"mask": mask, "kept": kept, "row_ptr": row_ptr, "total": int(total.value), "col_idx": None}
-    if csr:
-        col = torch.empty(max(1, total.value), dtype=torch.int32, device=dev)
-        mask_to_csr(mask, row_ptr, nb, col, ws=ws, stream=stream)
-        out["col_idx"] = col[:total.value]
-    return out
+
+    def call(ws, mask, kept, row_ptr, total, ptr):
+        return lib().prism_block_select(_ptr(qp), _ptr(kp), H, nb, d, float(scale), int(top_k), float(cdf_threshold),
+                                        _ptr(mask), _ptr(kept), _ptr(row_ptr), None, 0, ctypes.byref(total), ws.ptr,
+                                        ws.nbytes, ptr)
+
+    return _select(call, (qp, kp), ws, csr, stream, "prism_block_select")
 
 
 def block_select_ex(qp: torch.Tensor, kp: torch.Tensor, scale: float, top_k,
@@ -339,11 +431,8 @@ def block_select_ex(qp: torch.Tensor, kp: torch.Tensor, scale: float, top_k,
     [n_blocks] added to every head's logit of each key block (for example from
     ``block_audio_bias``). Returns the same dict as ``block_select``."""
     H, nb, d = qp.shape
-    words = (nb + 31) // 32
-    dev = qp.device
-    ws = (ws or Workspace(dev)).ensure(select_workspace_size(H, nb, d))
     cp = _SelectParams()
-    keep = []
+    keep, tensors = [], [qp, kp]
     if isinstance(top_k, (int,)) or (torch.is_tensor(top_k) and top_k.dim() == 0):
         cp.top_k = int(top_k)
     else:
@@ -361,19 +450,14 @@ def block_select_ex(qp: torch.Tensor, kp: torch.Tensor, scale: float, top_k,
     if key_bias is not None:
         assert key_bias.dtype == torch.float32 and key_bias.numel() == nb and key_bias.is_contiguous()
         cp.key_bias = key_bias.data_ptr()
-    mask = torch.empty((H, nb, words), dtype=torch.int32, device=dev)
-    kept = torch.empty((H, nb), dtype=torch.int32, device=dev)
-    row_ptr = torch.empty(H * nb + 1, dtype=torch.int32, device=dev)
-    total = _I64()
-    _check(lib().prism_block_select_ex(_ptr(qp), _ptr(kp), H, nb, d, float(scale), ctypes.byref(cp), _ptr(mask),
-                                       _ptr(kept), _ptr(row_ptr), None, 0, ctypes.byref(total), ws.ptr, ws.nbytes,
-                                       _stream(stream)), "prism_block_select_ex")
-    out = {"mask": mask, "kept": kept, "row_ptr": row_ptr, "total": int(total.value), "col_idx": None}
-    if csr:
-        col = torch.empty(max(1, total.value), dtype=torch.int32, device=dev)
-        mask_to_csr(mask, row_ptr, nb, col, ws=ws, stream=stream)
-        out["col_idx"] = col[:total.value]
-    return out
+        tensors.append(key_bias)
+
+    def call(ws, mask, kept, row_ptr, total, ptr):
+        return lib().prism_block_select_ex(_ptr(qp), _ptr(kp), H, nb, d, float(scale), ctypes.byref(cp), _ptr(mask),
+                                           _ptr(kept), _ptr(row_ptr), None, 0, ctypes.byref(total), ws.ptr, ws.nbytes,
+                                           ptr)
+
+    return _select(call, tensors, ws, csr, stream, "prism_block_select_ex")
 
 
 def topk_from_sparsity(sparsity: float, n_blocks: int) -> int:
@@ -389,12 +473,14 @@ def block_audio_bias(geo: Geometry, zone_shape: torch.Tensor, res: torch.Tensor,
     beta * (block mean of ||res[n]||) / (grid mean of ||res[n]||)."""
     _, nb = geo.counts()
     assert res.dim() == 2 and res.stride(1) == 1
-    ws = (ws or Workspace(res.device)).ensure(256)
-    out = torch.empty(nb, dtype=torch.float32, device=res.device)
+    what = "prism_block_audio_bias"
     g = geo.c()
-    _check(lib().prism_block_audio_bias(ctypes.byref(g), _ptr(zone_shape), _ptr(res), res.stride(0), res.shape[1],
-                                        _dtype_code(res), float(beta), _ptr(out), ws.ptr, ws.nbytes, _stream(stream)),
-           "prism_block_audio_bias")
+    with _On((zone_shape, res), stream, what) as on:
+        ws = on.workspace(ws, 256, what)
+        out = torch.empty(nb, dtype=torch.float32, device=res.device)
+        on.made(out)
+        _check(lib().prism_block_audio_bias(ctypes.byref(g), _ptr(zone_shape), _ptr(res), res.stride(0), res.shape[1],
+                                            _dtype_code(res), float(beta), _ptr(out), ws.ptr, ws.nbytes, on.ptr), what)
     return out
 
 
@@ -402,9 +488,11 @@ def mask_to_csr(mask: torch.Tensor, row_ptr: torch.Tensor, n_blocks: int, col_id
                 ws: Optional[Workspace] = None, stream=None):
     """Expands selection bitmask rows into ascending CSR column lists."""
     rows = row_ptr.numel() - 1
-    ws = (ws or Workspace(mask.device)).ensure(256)
-    _check(lib().prism_mask_to_csr(_ptr(mask), _ptr(row_ptr), rows, n_blocks, _ptr(col_idx), col_idx.numel(), ws.ptr,
-                                   ws.nbytes, _stream(stream)), "prism_mask_to_csr")
+    what = "prism_mask_to_csr"
+    with _On((mask, row_ptr, col_idx), stream, what) as on:
+        ws = on.workspace(ws, 256, what)
+        _check(lib().prism_mask_to_csr(_ptr(mask), _ptr(row_ptr), rows, n_blocks, _ptr(col_idx), col_idx.numel(),
+                                       ws.ptr, ws.nbytes, on.ptr), what)
     return col_idx
 
 
@@ -420,17 +508,25 @@ def bsa_fwd(geo: Geometry, zone_shape, q, k, v, scale, row_ptr, col_idx, ws: Opt
     N, H, d = q.shape
     assert q.stride(2) == 1 and q.stride(1) == d and k.stride() == q.stride() and v.stride() == q.stride()
     need = workspace_size("bsa_fwd", geo, heads=H, head_dim=d, dtype=q.dtype)
-    ws = (ws or Workspace(q.device)).ensure(need)
-    o = out if out is not None else torch.empty_like(q)
-    assert o.stride() == q.stride()
-    lse_t = lse if lse is not None else torch.empty((H, N), dtype=torch.float32, device=q.device)
+    what = "prism_bsa_fwd"
     if o_lo is not None:
         assert o_lo.dtype == torch.bfloat16 and o_lo.stride() == q.stride()
     g = geo.c()
-    _check(lib().prism_bsa_fwd(ctypes.byref(g), _ptr(zone_shape), _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), H, d,
-                               q.stride(0), float(scale), _ptr(row_ptr), _ptr(col_idx),
-                               -1 if nnz is None else int(nnz), _ptr(o), _ptr(lse_t),
-                               _ptr(o_lo), ws.ptr, ws.nbytes, _stream(stream)), "prism_bsa_fwd")
+    given = [t for t in (out, lse, o_lo) if t is not None]
+    with _On([zone_shape, q, k, v, row_ptr, col_idx, *given], stream, what) as on:
+        ws = on.workspace(ws, need, what)
+        o, lse_t = out, lse
+        if out is None:
+            o = torch.empty_like(q)
+            on.made(o)
+        assert o.stride() == q.stride()
+        if lse is None:
+            lse_t = torch.empty((H, N), dtype=torch.float32, device=q.device)
+            on.made(lse_t)
+        _check(lib().prism_bsa_fwd(ctypes.byref(g), _ptr(zone_shape), _ptr(q), _ptr(k), _ptr(v), _dtype_code(q), H, d,
+                                   q.stride(0), float(scale), _ptr(row_ptr), _ptr(col_idx),
+                                   -1 if nnz is None else int(nnz), _ptr(o), _ptr(lse_t),
+                                   _ptr(o_lo), ws.ptr, ws.nbytes, on.ptr), what)
     return o, lse_t
 
 
@@ -444,59 +540,26 @@ def bsa_bwd(geo: Geometry, zone_shape, q, k, v, o, lse, do, scale, row_ptr, col_
     for t in (k, v, o, do):
         assert t.stride() == q.stride()
     need = workspace_size("bsa_bwd", geo, heads=H, head_dim=d, dtype=q.dtype, nnz=nnz)
-    ws = (ws or Workspace(q.device)).ensure(need)
-    dq, dk, dv = grads if grads is not None else (torch.empty_like(q), torch.empty_like(q), torch.empty_like(q))
+    what = "prism_bsa_bwd"
     g = geo.c()
     if o_lo is not None:
         assert o_lo.dtype == torch.bfloat16 and o_lo.stride() == q.stride()
-    _check(lib().prism_bsa_bwd(ctypes.byref(g), _ptr(zone_shape), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_lo),
-                               _ptr(lse), _ptr(do), _dtype_code(q), H, d, q.stride(0), float(scale), _ptr(row_ptr),
-                               _ptr(col_idx), int(nnz), _ptr(dq), _ptr(dk), _ptr(dv), ws.ptr, ws.nbytes,
-                               _stream(stream)), "prism_bsa_bwd")
+    given = [t for t in (o_lo, *(grads or ())) if t is not None]
+    with _On([zone_shape, q, k, v, o, lse, do, row_ptr, col_idx, *given], stream, what) as on:
+        ws = on.workspace(ws, need, what)
+        if grads is None:
+            dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+            on.made(dq, dk, dv)
+        else:
+            dq, dk, dv = grads
+        _check(lib().prism_bsa_bwd(ctypes.byref(g), _ptr(zone_shape), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(o_lo),
+                                   _ptr(lse), _ptr(do), _dtype_code(q), H, d, q.stride(0), float(scale), _ptr(row_ptr),
+                                   _ptr(col_idx), int(nnz), _ptr(dq), _ptr(dk), _ptr(dv), ws.ptr, ws.nbytes, on.ptr),
+               what)
     return dq, dk, dv
 
 
 # ------------------------------------------------- around the attention
-def _require(ok: bool, what: str, status: int = 1):
-    if not ok:
-        raise PrismError(status, what)
-
-
-class _On:
-    """The device of a call's tensors made current, and the stream it runs on: the one given, or that device's
-    current one (`ptr`). Tensors that the call allocates for another stream are recorded on it (`made`)."""
-    __slots__ = ("guard", "stream", "foreign", "ptr")
-
-    def __init__(self, tensors, stream, what):
-        index = tensors[0].get_device()
-        for t in tensors:
-            if t.get_device() != index:
-                _require(False, what + ": tensors on different devices")
-        if index < 0:
-            _require(False, what + ": tensors must be on a CUDA device")
-        self.guard = None
-        if index != torch._C._cuda_getDevice():
-            self.guard = torch.cuda.device(index)
-            self.guard.__enter__()
-        own = torch._C._cuda_getCurrentRawStream(index)
-        self.stream = stream
-        self.ptr = own if stream is None else stream.cuda_stream
-        self.foreign = self.ptr != own
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def made(self, *tensors):
-        if self.foreign:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-
-
 _ROPE_LAYOUT = {"interleaved": 0, "half": 1}
 _ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -643,15 +706,6 @@ def _ffn_workspace_bytes(m, f, backward):
     return b.value
 
 
-def _ffn_workspace(ws, m, f, backward, device):
-    """The workspace, and its aligned start and the bytes from there."""
-    need = _ffn_workspace_bytes(m, f, backward)
-    buf = (ws or Workspace(device, need)).ensure(need).buf
-    p = buf.data_ptr()
-    start = (p + 255) // 256 * 256
-    return buf, start, buf.numel() - (start - p)
-
-
 def _new_like(t: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
     """A contiguous [rows, cols] matrix of t's type; t has that shape."""
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(rows, cols)
@@ -680,7 +734,7 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
     m = x.shape[0] if x.dim() else 0
     sx = _row_stride(x, m, d, what, "x")
     with _On(every, stream, what) as on:
-        buf, start, nbytes = _ffn_workspace(ws, m, f, 0, x.device)
+        ws = on.workspace(ws, _ffn_workspace_bytes(m, f, 0), what)
         y, gate, up, gp, upp = out, None, None, None, None
         if out is None:
             y = _new_like(x, m, d)
@@ -691,9 +745,9 @@ def gated_ffn_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_d
             gate = x.new_empty(m, f)
             up = x.new_empty(m, f)
             gp, upp = gate.data_ptr(), up.data_ptr()
-        on.made(y, gate, up, buf)
+        on.made(None if out is not None else y, gate, up)
         _check(lib().prism_gated_ffn_fwd(ctypes.byref(w), m, _ACT[act], code, x.data_ptr(), sx, y.data_ptr(), sy, gp, upp,
-                                         start, nbytes, on.ptr), what)
+                                         ws.start, ws.nbytes, on.ptr), what)
     return y, gate, up
 
 
@@ -714,7 +768,7 @@ def gated_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up:
         if t.shape != (m, f) or not t.is_contiguous():
             _require(False, what + ": gate and up must be contiguous [m, f]")
     with _On(every, stream, what) as on:
-        buf, start, nbytes = _ffn_workspace(ws, m, f, 1, x.device)
+        ws = on.workspace(ws, _ffn_workspace_bytes(m, f, 1), what)
         dx = dwg = dwu = dwd = xp = gp = upp = dp = None
         if need_dx:
             dx = _new_like(x, m, d)
@@ -722,9 +776,9 @@ def gated_ffn_bwd(dy: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up:
         if need_dw:
             dwg, dwu, dwd = _new_like(w_gate, f, d), _new_like(w_up, f, d), _new_like(w_down, d, f)
             gp, upp, dp = dwg.data_ptr(), dwu.data_ptr(), dwd.data_ptr()
-        on.made(dx, dwg, dwu, dwd, buf)
+        on.made(dx, dwg, dwu, dwd)
         _check(lib().prism_gated_ffn_bwd(ctypes.byref(w), m, _ACT[act], code, dy.data_ptr(), sdy, x.data_ptr(), sx,
-                                         gate.data_ptr(), up.data_ptr(), xp, d, gp, upp, dp, start, nbytes, on.ptr), what)
+                                         gate.data_ptr(), up.data_ptr(), xp, d, gp, upp, dp, ws.start, ws.nbytes, on.ptr), what)
     return dx, dwg, dwu, dwd
 
 
@@ -779,15 +833,15 @@ def _grad_list(grads, out=None) -> GradList:
     return GradList(grads, out)
 
 
-def _norm_call(grads, ws, device, stream, what):
-    if grads.device is None:
-        device = torch.device(device)
-        norm = torch.empty((), dtype=torch.float32, device=device)
-    else:
-        device = grads.device
-        norm = grads.grads[0].new_empty((), dtype=torch.float32)
-    ws = (ws or Workspace(device)).ensure(grads.workspace_bytes)
-    return norm, _On((norm,), stream, what), ws
+def _norm_call(grads, ws, device, stream, what, call):
+    """The norm that `call` (workspace, norm, stream) writes."""
+    tensors = grads.grads[:1] or [torch.empty(0, device=device)]
+    with _On(tensors, stream, what) as on:
+        ws = on.workspace(ws, grads.workspace_bytes, what)
+        norm = tensors[0].new_empty((), dtype=torch.float32)
+        on.made(norm)
+        _check(call(ws, norm.data_ptr(), on.ptr), what)
+    return norm
 
 
 def grad_norm(grads, ord=2, ws: Optional[Workspace] = None, device="cuda", stream=None) -> torch.Tensor:
@@ -795,12 +849,8 @@ def grad_norm(grads, ord=2, ws: Optional[Workspace] = None, device="cuda", strea
     an empty list only."""
     grads = _grad_list(grads)
     _require(ord in _NORM, f"prism_grad_norm: ord {ord!r}")
-    norm, on, ws = _norm_call(grads, ws, device, stream, "prism_grad_norm")
-    with on:
-        on.made(norm, ws.buf)
-        _check(lib().prism_grad_norm(grads._c, grads.n, _NORM[ord], norm.data_ptr(), ws.ptr, ws.nbytes, on.ptr),
-               "prism_grad_norm")
-    return norm
+    return _norm_call(grads, ws, device, stream, "prism_grad_norm", lambda ws, norm, ptr: lib().prism_grad_norm(
+        grads._c, grads.n, _NORM[ord], norm, ws.start, ws.nbytes, ptr))
 
 
 def scale_grads(grads, norm: torch.Tensor, max_norm: float, out=None, eps: float = 1e-6, stream=None):
@@ -819,12 +869,8 @@ def clip_grad_norm(grads, max_norm: float, ord=2, out=None, eps: float = 1e-6, w
     grads = _grad_list(grads, out)
     if ord not in _NORM:
         _require(False, f"prism_grad_clip: ord {ord!r}")
-    norm, on, ws = _norm_call(grads, ws, device, stream, "prism_grad_clip")
-    with on:
-        on.made(norm, ws.buf)
-        _check(lib().prism_grad_clip(grads._c, grads.n, _NORM[ord], float(max_norm), float(eps), norm.data_ptr(), ws.ptr,
-                                     ws.nbytes, on.ptr), "prism_grad_clip")
-    return norm
+    return _norm_call(grads, ws, device, stream, "prism_grad_clip", lambda ws, norm, ptr: lib().prism_grad_clip(
+        grads._c, grads.n, _NORM[ord], float(max_norm), float(eps), norm, ws.start, ws.nbytes, ptr))
 
 
 def default_scale(head_dim: int) -> float:

@@ -40,8 +40,11 @@
  *   "host" pointers are read (or written) before the call returns. The
  *   library never allocates or frees device memory: scratch comes from the
  *   caller's workspace `ws` of `ws_bytes` bytes (256-byte aligned), sized by
- *   prism_workspace_size(). Work is enqueued on `stream` (a cudaStream_t; NULL
- *   is the legacy default stream) and is asynchronous unless stated.
+ *   prism_workspace_size(). Its first 256 bytes, the device status word, have
+ *   to be zero before the first call that uses it (cleared in the order of that
+ *   call's stream); the rest needs no value. Work is enqueued on `stream` (a
+ *   cudaStream_t; NULL is the legacy default stream) and is asynchronous unless
+ *   stated.
  * - Every call validates its arguments on the host and returns a status; no
  *   exception crosses the ABI. Device-side faults are avoided by design:
  *   device waits are bounded and report PRISM_ERR_TIMEOUT, index checks
