@@ -64,6 +64,11 @@ bool meet(const void* a, int64_t lda, int64_t na, int64_t wa, const void* b, int
   return a0 < b1 && b0 < a1;
 }
 
+// `bytes` of the workspace, which every launch writes and reads, and a tensor.
+bool meet_ws(const void* ws, size_t bytes, const void* b, int64_t ldb, int64_t nb, int64_t wb) {
+  return meet(ws, 0, 1, int64_t(bytes / 2), b, ldb, nb, wb);
+}
+
 }  // namespace
 }  // namespace prism
 
@@ -91,7 +96,8 @@ extern "C" prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t 
   }
   if (!gate != !up) return PRISM_ERR_ARG;
   if (gate && (reinterpret_cast<uintptr_t>(gate) % 16 || reinterpret_cast<uintptr_t>(up) % 16)) return PRISM_ERR_ARG;
-  if ((st = check_ws(ws, ws_bytes, ffn_ws_bytes(m, f, false))) != PRISM_OK) return st;
+  const size_t need = ffn_ws_bytes(m, f, false);
+  if ((st = check_ws(ws, ws_bytes, need)) != PRISM_OK) return st;
   // what the first launch writes is not among what either reads, y not among what the first writes or the weights
   for (const void* o : {static_cast<const void*>(gate), static_cast<const void*>(up)}) {
     if (meet(o, f, m, f, x, x_stride, m, d) || meet(o, f, m, f, y, y_stride, m, d)) return PRISM_ERR_ARG;
@@ -99,7 +105,13 @@ extern "C" prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t 
       if (meet(o, f, m, f, rows[i].p, rows[i].ld, i < 2 ? f : d, rows[i].width)) return PRISM_ERR_ARG;
   }
   if (meet(gate, f, m, f, up, f, m, f)) return PRISM_ERR_ARG;
-  if (m > 0 && meet(y, y_stride, m, d, w->w_down, w->down_stride, d, f)) return PRISM_ERR_ARG;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t n = i < 2 ? f : d;
+    if (meet(y, y_stride, m, d, rows[i].p, rows[i].ld, n, rows[i].width)) return PRISM_ERR_ARG;
+    if (meet_ws(ws, need, rows[i].p, rows[i].ld, n, rows[i].width)) return PRISM_ERR_ARG;
+  }
+  if (meet_ws(ws, need, x, x_stride, m, d) || meet_ws(ws, need, y, y_stride, m, d)) return PRISM_ERR_ARG;
+  if (meet_ws(ws, need, gate, f, m, f) || meet_ws(ws, need, up, f, m, f)) return PRISM_ERR_ARG;
   if (m == 0) return PRISM_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void* h = static_cast<uint8_t*>(ws) + kWsHeader;
@@ -154,9 +166,10 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
       if ((st = check_rows(r)) != PRISM_OK) return st;
     if (dx && (st = check_rows({dx, dx_stride, d})) != PRISM_OK) return st;
   }
-  if ((st = check_ws(ws, ws_bytes, ffn_ws_bytes(m, f, true))) != PRISM_OK) return st;
+  const size_t need = ffn_ws_bytes(m, f, true);
+  if ((st = check_ws(ws, ws_bytes, need)) != PRISM_OK) return st;
   {
-    // no output over an input or another output
+    // no output over an input or another output, and nothing over the workspace
     const struct {
       const void* p;
       int64_t ld, n, width;
@@ -166,6 +179,8 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
     for (int i = 0; i < 4; ++i)
       for (int j = i + 1; j < 11; ++j)
         if (meet(t[i].p, t[i].ld, t[i].n, t[i].width, t[j].p, t[j].ld, t[j].n, t[j].width)) return PRISM_ERR_ARG;
+    for (const auto& r : t)
+      if (meet_ws(ws, need, r.p, r.ld, r.n, r.width)) return PRISM_ERR_ARG;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (m == 0) {  // sums over no token

@@ -452,6 +452,22 @@ prism_status check_apart(const prism_tensor* t, int64_t n, const float* norm) {
   return PRISM_OK;
 }
 
+// The norm and the workspace are written: neither may meet the other or a
+// gradient, nor the workspace a scaled one.
+prism_status check_written(const prism_tensor* t, int64_t n, const float* norm, const void* ws, size_t bytes, bool scaled) {
+  const uintptr_t m = reinterpret_cast<uintptr_t>(norm), w = reinterpret_cast<uintptr_t>(ws);
+  auto over = [](uintptr_t a, uintptr_t na, uintptr_t b, uintptr_t nb) { return a < b + nb && b < a + na; };
+  if (over(m, 4, w, bytes)) return PRISM_ERR_ARG;
+  for (int64_t i = 0; i < n; ++i) {
+    if (!t[i].numel) continue;
+    const uintptr_t size = uintptr_t(t[i].numel) * (t[i].dtype == PRISM_FP32 ? 4 : 2);
+    const uintptr_t s = reinterpret_cast<uintptr_t>(t[i].data), d = reinterpret_cast<uintptr_t>(t[i].out);
+    if (over(s, size, w, bytes) || over(s, size, m, 4)) return PRISM_ERR_ARG;
+    if (scaled && d && (over(d, size, w, bytes) || over(d, size, m, 4))) return PRISM_ERR_ARG;
+  }
+  return PRISM_OK;
+}
+
 int64_t chunks_of(const prism_tensor& t) {
   const int64_t bytes = t.numel * (t.dtype == PRISM_FP32 ? 4 : 2) + int64_t(reinterpret_cast<uintptr_t>(t.data) % 16);
   return (bytes + kGnChunkVecs * 16 - 1) / (kGnChunkVecs * 16);
@@ -569,6 +585,7 @@ extern "C" prism_status prism_grad_norm(const prism_tensor* grads, int64_t n_ten
   if (ord != PRISM_NORM_L2 && ord != PRISM_NORM_INF) return PRISM_ERR_ARG;
   prism_status st = check_tensors(grads, n_tensors, false);
   if (st == PRISM_OK) st = check_norm_ws(ws, ws_bytes, n_tensors);
+  if (st == PRISM_OK) st = check_written(grads, n_tensors, norm, ws, norm_ws_bytes(n_tensors), false);
   if (st != PRISM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const GnScale small = {nullptr, 0, ord == PRISM_NORM_INF, norm, 1, 0.f, 0.f};
@@ -597,6 +614,7 @@ extern "C" prism_status prism_grad_clip(const prism_tensor* grads, int64_t n_ten
   if (ord != PRISM_NORM_L2 && ord != PRISM_NORM_INF) return PRISM_ERR_ARG;
   prism_status st = check_tensors(grads, n_tensors, true);
   if (st == PRISM_OK) st = check_norm_ws(ws, ws_bytes, n_tensors);
+  if (st == PRISM_OK) st = check_written(grads, n_tensors, norm, ws, norm_ws_bytes(n_tensors), true);
   if (st == PRISM_OK) st = check_apart(grads, n_tensors, norm);
   if (st != PRISM_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

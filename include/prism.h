@@ -513,7 +513,8 @@ typedef struct {
  *
  * grads: host array of n_tensors (0 .. 2^20) entries; a tensor listed twice
  *       counts twice. norm: device float out.
- * ws: at least prism_grad_norm_workspace_size(n_tensors) bytes.
+ * ws: at least prism_grad_norm_workspace_size(n_tensors) bytes. Norm and
+ *       workspace share no memory with each other or a tensor (PRISM_ERR_ARG).
  * A step whose gradients are split over ranks (a layer sharded by heads) adds
  * up norm^2 over the ranks between prism_grad_norm and prism_grad_scale.
  */
@@ -569,7 +570,8 @@ typedef struct {
  * projections and rounded to bf16 once, as an operand of the second product (of
  * at most 32 tokens it is kept to 16 bits and more, as two operands: an infinite
  * weight or input may then give NaN where one operand gives an infinity).
- * No output may share memory with gate, up or the weights; y may be x.
+ * No output may share memory with gate, up or the weights, and no tensor with
+ * the workspace (PRISM_ERR_ARG); y may be x.
  * ws: at least prism_gated_ffn_workspace_size(m, f, 0) bytes (the status word
  *       and h).
  */
@@ -585,7 +587,8 @@ PRISM_API prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t m
  * dw_down = dy^T (act(gate) up). relu'(0) = 0.
  * dx: device [m, d] out, or NULL. dw_gate, dw_up [f, d], dw_down [d, f]: device
  *       contiguous outs, or all NULL (frozen weights). m = 0 zeroes them.
- * No output may share memory with any other tensor of the call.
+ * No output may share memory with any other tensor of the call, and none with
+ * the workspace (PRISM_ERR_ARG).
  * ws: at least prism_gated_ffn_workspace_size(m, f, 1) bytes (the status word,
  *       dg, du and act(gate) up).
  */

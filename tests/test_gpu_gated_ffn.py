@@ -336,3 +336,33 @@ def test_refusals():
                  (x, wg, wu, wd[:, ::2])):
         with pytest.raises(P.PrismError):
             P.gated_ffn_fwd(*args)
+
+
+def test_refusals_of_shared_memory():
+    """y over any weight, and any tensor over the workspace, are refused before any CUDA call."""
+    from dynamic_block_sparse_shape_b200 import build
+    build.build()
+    lib, w = P.lib(), _weights()
+    A, far = 1 << 30, 1 << 34
+    need = {}
+    for backward in (0, 1):
+        b = ctypes.c_size_t()
+        assert lib.prism_gated_ffn_workspace_size(4, 128, backward, ctypes.byref(b)) == 0
+        need[backward] = b.value
+
+    def fwd(x=A, y=A + (1 << 16), gate=A + (2 << 16), up=A + (3 << 16), ws=far):
+        return lib.prism_gated_ffn_fwd(ctypes.byref(w), 4, 0, 0, x, 64, y, 64, gate, up, ws, 1 << 40, None)
+
+    def bwd(dy=A, x=A + (1 << 16), gate=A + (2 << 16), up=A + (3 << 16), dx=A + (4 << 16), g=A + (5 << 16),
+            u=A + (6 << 16), d=A + (7 << 16), ws=far):
+        return lib.prism_gated_ffn_bwd(ctypes.byref(w), 4, 0, 0, dy, 64, x, 64, gate, up, dx, 64, g, u, d, ws, 1 << 40, None)
+
+    for weight, last in ((1 << 20, 128 * 128 - 16), (1 << 22, 128 * 128 - 16), (1 << 24, 64 * 256 - 16)):
+        for y in (weight, weight + last, weight - 16):
+            assert fwd(y=y) == 1
+        for ws in (weight, weight - 256):
+            assert fwd(ws=ws) == 1 and bwd(ws=ws) == 1
+    for call, names, n in ((fwd, ("x", "y", "gate", "up"), need[0]),
+                           (bwd, ("dy", "x", "gate", "up", "dx", "g", "u", "d"), need[1])):
+        for name in names:  # over the first and the last bytes that the call uses
+            assert call(**{name: far}) == 1 and call(**{name: far + n - 16}) == 1

@@ -227,3 +227,21 @@ def test_refusals():
         P.GradList([torch.zeros(4, dtype=torch.float16)])
     with pytest.raises(P.PrismError):
         P.grad_norm([torch.zeros(4)], ord=3)
+
+
+def test_refusals_of_shared_memory():
+    """The norm or the workspace over a tensor or over one another, before any CUDA call."""
+    from dynamic_block_sparse_shape_b200 import build
+    build.build()
+    ws, norm, big = 1 << 24, 1 << 20, 1 << 30
+    b = ctypes.c_size_t()
+    assert P.lib().prism_grad_norm_workspace_size(1, ctypes.byref(b)) == 0
+    calls = [lambda e, n=norm: _raw("prism_grad_norm", e, 0, n, ws, big, None),
+             lambda e, n=norm: _raw("prism_grad_clip", e, 0, 1.0, 1e-6, n, ws, big, None)]
+    for call in calls:
+        for at in (ws, ws - 196, ws + b.value - 4):
+            assert call([(at, None, 100, 0, 0)]) == 1
+        assert call([(norm, None, 100, 0, 0)]) == 1 and call([(norm - 196, None, 100, 0, 0)]) == 1
+        assert call([(1 << 21, None, 100, 0, 0)], ws + 4) == 1 and call([], ws + b.value - 4) == 1
+    for at in (ws, ws - 196, ws + b.value - 4, norm):
+        assert calls[1]([(1 << 21, at, 100, 0, 0)]) == 1  # where the scaled values go
