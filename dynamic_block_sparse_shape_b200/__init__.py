@@ -633,7 +633,8 @@ def _rope(q, k, spec, grid, positions, out, stream, transposed, what):
     if positions is not None:
         if positions.dtype != torch.int32:
             _require(False, what + ": positions must be int32", 3)
-        if positions.numel() != n * len(spec.axis_dims) or not positions.is_contiguous():
+        axes = len(spec.axis_dims)
+        if positions.numel() != n * axes or (axes > 1 and positions.shape != (n, axes)) or not positions.is_contiguous():
             _require(False, what + ": positions must be contiguous [tokens, axes]")
         tensors.append(positions)
         pp = positions.data_ptr()
@@ -664,7 +665,8 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], spec: RopeSpec, grid=None,
          positions: Optional[torch.Tensor] = None, out=None, stream=None):
     """Rotary positions of Q [N, heads, d] and K [N, heads_k, d] (or None): returns the rotated (q, k).
 
-    grid: the (T, H, W) token grid in raster order, for a three-axis spec; positions: int32 [N, axes] instead of it.
+    grid: the (T, H, W) token grid in raster order, for a three-axis spec; positions: int32 [N, axes] instead of it
+    (one axis: N values of any shape).
     With neither, a one-axis spec takes the token's index. out: the pair of tensors to write, (q, k) for in place."""
     return _rope(q, k, spec, grid, positions, out, stream, 0, "prism_rope")
 

@@ -255,3 +255,19 @@ def test_refusals():
         P.RopeSpec((64, 2))
     with pytest.raises(P.PrismError):  # not on a GPU
         P.rope(torch.zeros(1, 1, 64), None, P.RopeSpec((64,)))
+
+
+@pytest.mark.parametrize("call", [P.rope, P.rope_bwd])
+def test_refusals_of_positions(call):
+    """Positions of three axes come as [tokens, axes]: the same number of values in another shape is not taken."""
+    x, spec = torch.zeros(5, 2, 16), P.RopeSpec((4, 4, 4))
+    good = torch.zeros(5, 3, dtype=torch.int32)
+    for bad in (good.t().contiguous(), good.view(15), good.view(1, 5, 3), good[:4], good.t().contiguous().t()):
+        with pytest.raises(P.PrismError, match="positions"):
+            call(x, None, spec, positions=bad)
+    with pytest.raises(P.PrismError, match="positions"):
+        call(x, None, spec, positions=good.long())
+    one = P.RopeSpec((8,))
+    for fine, s in ((good, spec), (good[:, 0].contiguous(), one), (torch.zeros(1, 5, dtype=torch.int32), one)):
+        with pytest.raises(P.PrismError, match="CUDA device"):  # taken as far as that goes without a GPU
+            call(x, None, s, positions=fine)
