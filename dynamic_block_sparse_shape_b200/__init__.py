@@ -95,6 +95,8 @@ _SIGNATURES = {
     "prism_workspace_size": (ctypes.c_int, [ctypes.c_int, _GEO, _I32, _I32, _I32, _I32, ctypes.c_int, _I64,
                                             ctypes.POINTER(_SZ)]),
     "prism_check_device_status": (ctypes.c_int, [_P, _P]),
+    "prism_keep_device_status": (ctypes.c_int, [_P, _P]),
+    "prism_check_kept_status": (ctypes.c_int, [_P, _P]),
     "prism_zone_shapes": (ctypes.c_int, [_GEO, _P, _I64, _I32, ctypes.c_int, _P, _I64, _I32, ctypes.c_int,
                                          ctypes.POINTER(_ShapeParams), _P, _P, _P, _SZ, _P]),
     "prism_zone_shapes_static": (ctypes.c_int, [_GEO, _P, _I64, _I32, ctypes.c_int, _P, _I64, _I32, ctypes.c_int,
@@ -280,7 +282,7 @@ class _On:
     """The device and the stream of a call made current: those of its tensors (of the current device without any), and
     the stream given or that device's current one (`ptr`). What the call allocates then belongs to its stream; results
     are noted on the caller's stream as well (`made`), which goes on to read them."""
-    __slots__ = ("guard", "caller", "ptr", "device")
+    __slots__ = ("guard", "caller", "ptr", "device", "passing")
 
     def __init__(self, tensors, stream, what):
         index = tensors[0].get_device() if tensors else torch.cuda.current_device()
@@ -290,7 +292,7 @@ class _On:
         if index < 0:
             _require(False, what + ": tensors must be on a CUDA device")
         self.device = index
-        self.guard = self.caller = None
+        self.guard = self.caller = self.passing = None
         self.ptr = _raw_stream(index)
         if stream is not None and stream.cuda_stream != self.ptr:
             _require(stream.device_index == index, what + ": a stream of another device")
@@ -306,8 +308,13 @@ class _On:
         return self
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        try:
+            if self.passing is not None and exc[0] is None:
+                # the workspace goes, what its status word says stays
+                _check(lib().prism_keep_device_status(self.passing.start, self.ptr), "device status")
+        finally:
+            if self.guard is not None:
+                self.guard.__exit__(*exc)
 
     def made(self, *tensors):
         if self.caller is not None:
@@ -318,15 +325,23 @@ class _On:
     def workspace(self, ws: Optional[Workspace], nbytes: int, what: str) -> Workspace:
         """The workspace given, or one for this call, with room for `nbytes`."""
         if ws is None:
-            return Workspace(torch.device("cuda", self.device), nbytes)
+            self.passing = Workspace(torch.device("cuda", self.device), nbytes)
+            return self.passing
         if ws.buf.get_device() != self.device:
             _require(False, what + ": a workspace of another device", 4)
         return ws.ensure(nbytes)
 
 
-def check_device_status(ws: Workspace, stream=None):
-    with _On([ws.buf], stream, "device status") as on:
-        _check(lib().prism_check_device_status(ws.ptr, on.ptr), "device status")
+def check_device_status(ws: Optional[Workspace] = None, stream=None):
+    """Waits for the stream and raises what a kernel that used ``ws`` reported: a wait that ran out, a bad index. Without
+    ``ws``: what the calls without a workspace on the current device did."""
+    what = "device status"
+    with _On([ws.buf] if ws is not None else [], stream, what) as on:
+        if ws is not None:
+            _check(lib().prism_check_device_status(ws.ptr, on.ptr), what)
+        else:
+            tmp = Workspace(torch.device("cuda", on.device), 256)
+            _check(lib().prism_check_kept_status(tmp.ptr, on.ptr), what)
 
 
 def zone_shapes(geo: Geometry, feat: Optional[torch.Tensor] = None, res: Optional[torch.Tensor] = None,

@@ -154,6 +154,31 @@ extern "C" prism_status prism_workspace_size(prism_op op, const prism_geometry* 
   return PRISM_ERR_ARG;
 }
 
+// What calls reported whose workspaces are gone (prism_keep_device_status).
+namespace prism {
+namespace {
+static __device__ int g_kept_status;
+
+__global__ void keep_status_kernel(const int* status) {
+  if (const int s = *status) atomicOr(&g_kept_status, s);
+}
+__global__ void take_status_kernel(int* out) { *out = atomicExch(&g_kept_status, 0); }
+}  // namespace
+}  // namespace prism
+
+extern "C" prism_status prism_keep_device_status(const void* ws, void* stream) {
+  if (!ws) return PRISM_ERR_WORKSPACE;
+  keep_status_kernel<<<1, 1, 0, reinterpret_cast<cudaStream_t>(stream)>>>(static_cast<const int*>(ws));
+  return cuda_status(cudaGetLastError());
+}
+
+extern "C" prism_status prism_check_kept_status(void* ws, void* stream) {
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return PRISM_ERR_WORKSPACE;
+  take_status_kernel<<<1, 1, 0, reinterpret_cast<cudaStream_t>(stream)>>>(static_cast<int*>(ws));
+  if (cudaGetLastError() != cudaSuccess) return PRISM_ERR_CUDA;
+  return prism_check_device_status(ws, stream);
+}
+
 extern "C" prism_status prism_check_device_status(void* ws, void* stream) {
   if (!ws) return PRISM_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

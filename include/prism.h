@@ -136,6 +136,15 @@ PRISM_API prism_status prism_workspace_size(prism_op op, const prism_geometry* g
  * used this workspace reported one, else PRISM_OK. */
 PRISM_API prism_status prism_check_device_status(void* ws, void* stream);
 
+/* For a caller that gives its workspace up after a call: adds the status word
+ * of `ws` (256 bytes read, in the order of `stream`) to one that the library
+ * keeps on the current device. */
+PRISM_API prism_status prism_keep_device_status(const void* ws, void* stream);
+
+/* prism_check_device_status of what was kept, over all streams, for the work
+ * that `stream` is behind. ws: a free workspace of 256 bytes; cleared. */
+PRISM_API prism_status prism_check_kept_status(void* ws, void* stream);
+
 /*
  * a1 + a2 — macro-zone tiling and per-zone block shape.
  * Cites: README "Overview" (zones; video feature variance along the channel

@@ -48,3 +48,12 @@ def test_a_workspace_of_another_device_is_refused():
     with pytest.raises(P.PrismError) as e:
         call.workspace(P.Workspace("cpu"), 1024, "a call")
     assert e.value.status == 4
+
+
+def test_refusals_of_kept_status():
+    """Host checks of the status calls, before any CUDA call."""
+    from dynamic_block_sparse_shape_b200 import build
+    build.build()
+    assert P.lib().prism_keep_device_status(None, None) == 4
+    assert P.lib().prism_check_kept_status(None, None) == 4
+    assert P.lib().prism_check_kept_status(8, None) == 4
