@@ -187,7 +187,8 @@ __device__ __forceinline__ void act_slope_f(float g, float& a, float& slope) {
   } else if constexpr (ACT == PRISM_ACT_GELU_TANH) {
     const float s = sigmoid_f(1.5957691216057308f * (g + 0.044715f * g * g * g));
     a = g * s;
-    slope = s + a * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * g * g);
+    // s is 0 or 1 from |g| = 11 on, and 0 times an overflowed square would be NaN
+    slope = s + a * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * fminf(g * g, 1e30f));
   } else {
     a = g <= 0.f ? 0.f : g;
     slope = g > 0.f ? 1.f : 0.f;

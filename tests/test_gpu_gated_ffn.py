@@ -366,3 +366,31 @@ def test_refusals_of_shared_memory():
                            (bwd, ("dy", "x", "gate", "up", "dx", "g", "u", "d"), need[1])):
         for name in names:  # over the first and the last bytes that the call uses
             assert call(**{name: far}) == 1 and call(**{name: far + n - 16}) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m", [8, 20, 40, 300])
+def test_far_projections(m, act):
+    """Projections up to the type's largest: the activation is g or 0 there and its slope 1 or 0, never NaN from a power
+    of g that overflows."""
+    require_gpu()
+    far = torch.tensor([0.0, -0.0, 3.0, -3.0, 1e12, -1e12, 1.7e19, -1.7e19, 1e25, -1e25, 3e38, -3e38, 1e-30, -1e-30],
+                       dtype=torch.bfloat16)
+    g = far[torch.arange(m) % len(far)]
+    eye = torch.eye(8, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(m, 8, dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = g, 1.0
+    wg, wu = torch.zeros(8, 8, dtype=torch.bfloat16), torch.zeros(8, 8, dtype=torch.bfloat16)
+    wg[:, 0], wu[:, 1] = 1.0, 0.5
+    y, gate, up = P.gated_ffn_fwd(x.cuda(), wg.cuda(), wu.cuda(), eye, act=act)
+    assert torch.equal(gate, g.cuda()[:, None].expand(m, 8)) and (up == 0.5).all()
+    a, slope = O.activation(act, f64(gate)), O.activation_slope(act, f64(gate))
+    # the exponential's 2^-20 (1 + |g|) counts where it is not saturated; one rounding of h and one of y
+    tol = (2.0 ** -20 * (1 + np.minimum(np.abs(f64(gate)), 200.0)) + 2 * STEP * (1 + STEP)) * np.abs(a * 0.5) + 2.0 ** -120
+    assert (np.abs(f64(y) - a * 0.5) <= tol).all()
+    dy = torch.full((m, 8), 2.0 ** -4, dtype=torch.bfloat16, device="cuda")
+    dx = P.gated_ffn_bwd(dy, x.cuda(), eye, torch.zeros_like(eye), eye, gate, up, act=act, need_dw=False)[0]
+    want = 2.0 ** -4 * 0.5 * slope
+    tol = (2.0 ** -19 * (1 + 9.0) + 2 * STEP * (1 + STEP)) * np.maximum(np.abs(want), 2.0 ** -6) + 2.0 ** -120
+    assert (np.abs(f64(dx) - want) <= tol).all()
