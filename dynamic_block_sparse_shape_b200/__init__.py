@@ -588,7 +588,7 @@ class RopeSpec:
     theta: pair j of an axis of n channels turns by theta ** (-2 j / n) per position.
     scaling, factor, trained_len: "none"; "linear" (frequencies / factor); "ntk" (theta * factor ** (n / (n - 2)));
         "yarn" (pairs that turn over 32 times in trained_len positions kept, those below once / factor, a ramp between).
-    magnitude: multiplies the rotated channels; None is 1, or 0.1 ln(factor) + 1 with "yarn".
+    magnitude: multiplies the rotated channels; None is 1, or 0.1 ln(factor) + 1 with "yarn" and a factor above 1.
     pos_scale, pos_offset: per axis, the position p counts as pos_offset + p * pos_scale (for example video frames on
         the time axis of the audio tokens).
     """
@@ -601,7 +601,7 @@ class RopeSpec:
         _require(scaling in _ROPE_SCALING, f"RopeSpec: scaling {scaling!r}")
         if magnitude is None:
             _require(scaling != "yarn" or factor > 0, "RopeSpec: factor must be positive")
-            magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
+            magnitude = 0.1 * math.log(max(factor, 1.0)) + 1.0 if scaling == "yarn" else 1.0
         scale = tuple(pos_scale) if pos_scale is not None else (1.0,) * len(dims)
         offset = tuple(pos_offset) if pos_offset is not None else (0.0,) * len(dims)
         _require(len(scale) == len(dims) and len(offset) == len(dims), "RopeSpec: one pos_scale and pos_offset per axis")

@@ -271,3 +271,13 @@ def test_refusals_of_positions(call):
     for fine, s in ((good, spec), (good[:, 0].contiguous(), one), (torch.zeros(1, 5, dtype=torch.int32), one)):
         with pytest.raises(P.PrismError, match="CUDA device"):  # taken as far as that goes without a GPU
             call(x, None, s, positions=fine)
+
+
+def test_magnitude_of_a_stretched_context():
+    """0.1 ln(factor) + 1 belongs to stretched contexts; one that is not stretched, or shortened, keeps its magnitude."""
+    for factor, want in ((8.0, 0.1 * np.log(8.0) + 1), (1.0, 1.0), (0.5, 1.0), (1e-6, 1.0)):
+        assert abs(P.RopeSpec((8,), scaling="yarn", factor=factor).magnitude - want) < 1e-15
+    assert P.RopeSpec((8,), scaling="yarn", factor=0.5, magnitude=0.75).magnitude == 0.75
+    assert P.RopeSpec((8,), scaling="linear", factor=8.0).magnitude == 1.0
+    with pytest.raises(P.PrismError):
+        P.RopeSpec((8,), scaling="yarn", factor=0.0)
