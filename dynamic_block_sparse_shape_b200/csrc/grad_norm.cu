@@ -289,10 +289,11 @@ struct GnScale {
   float max_norm, eps;
 };
 
-// A NaN norm makes every value NaN, unless there is nothing to clip to.
+// A NaN norm makes every value NaN, unless there is nothing to clip to; a norm
+// of 0 (and eps = 0) leaves the values, with a bound of 0 too.
 __device__ __forceinline__ float clip_factor(const GnScale& S, double norm) {
-  const double f = double(S.max_norm) / (norm + double(S.eps));
-  return f >= 1.0 || isinf(S.max_norm) ? 1.f : float(f);
+  const double by = norm + double(S.eps), f = double(S.max_norm) / by;
+  return f >= 1.0 || by == 0.0 || isinf(S.max_norm) ? 1.f : float(f);
 }
 
 // Pass 2: the factor, and this CTA's chunks times it, last chunk first.

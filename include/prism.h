@@ -538,7 +538,7 @@ PRISM_API prism_status prism_grad_norm_workspace_size(int64_t n_tensors, size_t*
  * from device memory (rounded once to its type). A factor of 1 leaves in-place
  * tensors untouched; a NaN norm makes every value NaN, an infinite one makes
  * finite values 0. max_norm >= 0 (infinity: the factor is 1 whatever the norm);
- * eps >= 0. No tensor's output may share memory with the norm, with another
+ * eps >= 0 (with norm + eps = 0 the factor is 1). No tensor's output may share memory with the norm, with another
  * tensor of the list or, other than exactly, with its own input (PRISM_ERR_ARG).
  */
 PRISM_API prism_status prism_grad_scale(const prism_tensor* grads, int64_t n_tensors, const float* norm,

@@ -245,3 +245,19 @@ def test_refusals_of_shared_memory():
         assert call([(1 << 21, None, 100, 0, 0)], ws + 4) == 1 and call([], ws + b.value - 4) == 1
     for at in (ws, ws - 196, ws + b.value - 4, norm):
         assert calls[1]([(1 << 21, at, 100, 0, 0)]) == 1  # where the scaled values go
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [100, 300000])
+def test_nothing_to_scale_by(n):
+    """A norm of 0 and eps = 0 leave the values whatever the bound, 0 among them: no 0 / 0."""
+    require_gpu()
+    for limit in (0.0, 1.0):
+        z = [torch.zeros(n, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda")]
+        assert float(P.clip_grad_norm(z, limit, eps=0.0)) == 0.0 and all((t == 0).all() for t in z)
+        one = [torch.ones(n, device="cuda")]
+        P.scale_grads(one, torch.zeros((), device="cuda"), limit, eps=0.0)
+        assert (one[0] == 1).all()
+    one = [torch.ones(n, device="cuda")]
+    P.clip_grad_norm(one, 0.0, eps=0.0)
+    assert (one[0] == 0).all()
