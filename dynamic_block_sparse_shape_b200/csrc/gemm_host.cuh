@@ -232,7 +232,8 @@ inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, 
   double best = k * (whole * both + (rest > 0 ? (rest * 2 <= pairs ? one : both) : 0.0)) + kPersistentNs;
   GemmChoice c = {2, 0, 1};
   if (single) best = HUGE_VAL;
-  const GemmChoice tries[] = {{1, 64, 8}, {1, 128, 4}, {2, 256, 4}};  // with the most parts
+  // with the most parts that shared memory has room for: of four parts of a pair's tile not even the sums fit
+  const GemmChoice tries[] = {{1, 64, 8}, {1, 128, 4}, {2, 256, 2}};
   for (const GemmChoice& t : tries) {
     if (single && t.cg == 2) continue;
     const int rows_a = a_mn || t.cg == 2 || m[0] >= kGemmM ? kGemmM : int(m[0] + 7) / 8 * 8;
