@@ -120,6 +120,7 @@ _SIGNATURES = {
                                            _P, _P, _SZ, _P]),
     "prism_gated_ffn_bwd": (ctypes.c_int, [ctypes.POINTER(_FfnWeights), _I64, _I32, ctypes.c_int, _P, _I64, _P, _I64, _P,
                                            _P, _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "prism_gated_ffn_forms": (ctypes.c_int, [ctypes.POINTER(_FfnWeights), _I64, _I32, ctypes.POINTER(_I32)]),
     "prism_gated_ffn_workspace_size": (ctypes.c_int, [_I64, _I32, _I32, ctypes.POINTER(_SZ)]),
     "prism_grad_norm": (ctypes.c_int, [_P, _I64, _I32, _P, _P, _SZ, _P]),
     "prism_grad_norm_workspace_size": (ctypes.c_int, [_I64, ctypes.POINTER(_SZ)]),

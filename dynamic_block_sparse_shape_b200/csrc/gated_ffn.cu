@@ -69,6 +69,106 @@ bool meet_ws(const void* ws, size_t bytes, const void* b, int64_t ldb, int64_t n
   return meet(ws, 0, 1, int64_t(bytes / 2), b, ldb, nb, wb);
 }
 
+// The launches of a checked call; with `form` none, but what each would take.
+prism_status run_fwd(const prism_ffn_weights& w, int64_t m, int32_t act, const void* x, int64_t x_stride, void* y,
+                     int64_t y_stride, void* gate, void* up, void* ws, cudaStream_t s, GemmChoice* form) {
+  const int32_t d = w.d, f = w.f;
+  prism_status st;
+  void* h = static_cast<uint8_t*>(ws) + kWsHeader;
+  if (ffn_takes_rows(m, d)) return form ? PRISM_OK : ffn_rows_forward(act, w, int(m), x, x_stride, h, y, y_stride, gate, up, s);
+  GemmArgs P;
+  std::memset(&P, 0, sizeof(P));
+  P.status = ws_status(ws);
+  P.save = gate != nullptr;
+  GemmProblem g;
+  g.a[0] = {x, x_stride};
+  g.b[0] = {w.w_gate, w.gate_stride};
+  g.b[1] = {w.w_up, w.up_stride};
+  g.out[0] = {h, f};
+  g.out[1] = {gate, f};
+  g.out[2] = {up, f};
+  g.m = m; g.n = f; g.k[0] = d;
+  const bool fine = m <= kFineTokens;
+  P.fine = fine;
+  if ((st = ffn_gate_product(act, P, g, s, form)) != PRISM_OK) return st;
+  GemmProblem r;
+  r.a[0] = {h, f};
+  r.b[0] = {w.w_down, w.down_stride};
+  r.out[0] = {y, y_stride};
+  r.m = fine ? 2 * m : m;  // the values' rows, then the remainders': added to one another at the end
+  r.n = d; r.k[0] = f;
+  P.follows = 1;
+  P.fine = 0;
+  P.fold = fine ? int(m) : 0;
+  return ffn_product_nt(P, r, s, form ? form + 1 : nullptr);
+}
+
+prism_status run_bwd(const prism_ffn_weights& w, int64_t m, int32_t act, const void* dy, int64_t dy_stride, const void* x,
+                     int64_t x_stride, const void* gate, const void* up, void* dx, int64_t dx_stride, void* dw_gate,
+                     void* dw_up, void* dw_down, void* ws, cudaStream_t s, GemmChoice* form) {
+  const int32_t d = w.d, f = w.f;
+  const bool dw = dw_gate != nullptr;
+  prism_status st;
+  const size_t part = ffn_part_bytes(m, f);
+  const bool fine = m <= kFineTokens;
+  uint8_t* base = static_cast<uint8_t*>(ws) + kWsHeader;
+  void *dg = base, *du = base + part, *h = base + 2 * part;
+  GemmArgs P;
+  std::memset(&P, 0, sizeof(P));
+  P.status = ws_status(ws);
+  P.save = dw;
+  GemmProblem g;
+  g.a[0] = {dy, dy_stride};
+  g.in[0] = gate;
+  g.in[1] = up;
+  g.b[0] = {w.w_down, w.down_stride};
+  g.out[0] = {dg, f};
+  g.out[1] = {du, f};
+  g.out[2] = {h, f};
+  g.m = m; g.n = f; g.k[0] = d;
+  P.fine = fine;
+  if ((st = ffn_gate_bwd_product(act, P, g, s, form)) != PRISM_OK) return st;
+  P.follows = 1;
+  P.fine = 0;
+  if (dx) {
+    GemmProblem r;
+    r.a[0] = {dg, f};
+    r.a[1] = {du, f};
+    r.b[0] = {w.w_gate, w.gate_stride};
+    r.b[1] = {w.w_up, w.up_stride};
+    r.out[0] = {dx, dx_stride};
+    r.m = fine ? 2 * m : m;  // folded as in the forward
+    r.n = d; r.k[0] = f; r.k[1] = f;
+    P.fold = fine ? int(m) : 0;
+    if ((st = ffn_product_nn(P, r, s, form ? form + 1 : nullptr)) != PRISM_OK) return st;
+    P.fold = 0;
+  }
+  if (dw) {
+    GemmProblem r[3];
+    const void* a[3] = {dg, du, dy};
+    void* o[3] = {dw_gate, dw_up, dw_down};
+    for (int i = 0; i < 3; ++i) {
+      r[i].a[0] = {a[i], i < 2 ? f : dy_stride};
+      r[i].b[0] = {i < 2 ? x : h, i < 2 ? x_stride : f};
+      r[i].out[0] = {o[i], i < 2 ? d : f};
+      r[i].m = i < 2 ? f : d;
+      r[i].n = i < 2 ? d : f;
+      r[i].k[0] = m;
+      if (fine) {  // the remainders as a second segment of K
+        const int64_t below = m * f;
+        r[i].a[1] = r[i].a[0];
+        r[i].b[1] = r[i].b[0];
+        GemmOperand& o2 = i < 2 ? r[i].a[1] : r[i].b[1];
+        o2.base = static_cast<const __nv_bfloat16*>(o2.base) + below;
+        r[i].k[1] = m;
+      }
+    }
+    P.beside = dx != nullptr;
+    if ((st = ffn_products_tn(P, r, 3, s, form ? form + 2 : nullptr)) != PRISM_OK) return st;
+  }
+  return PRISM_OK;
+}
+
 }  // namespace
 }  // namespace prism
 
@@ -113,34 +213,7 @@ extern "C" prism_status prism_gated_ffn_fwd(const prism_ffn_weights* w, int64_t 
   if (meet_ws(ws, need, x, x_stride, m, d) || meet_ws(ws, need, y, y_stride, m, d)) return PRISM_ERR_ARG;
   if (meet_ws(ws, need, gate, f, m, f) || meet_ws(ws, need, up, f, m, f)) return PRISM_ERR_ARG;
   if (m == 0) return PRISM_OK;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  void* h = static_cast<uint8_t*>(ws) + kWsHeader;
-  if (ffn_takes_rows(m, d)) return ffn_rows_forward(act, *w, int(m), x, x_stride, h, y, y_stride, gate, up, s);
-  GemmArgs P;
-  std::memset(&P, 0, sizeof(P));
-  P.status = ws_status(ws);
-  P.save = gate != nullptr;
-  GemmProblem g;
-  g.a[0] = {x, x_stride};
-  g.b[0] = {w->w_gate, w->gate_stride};
-  g.b[1] = {w->w_up, w->up_stride};
-  g.out[0] = {h, f};
-  g.out[1] = {gate, f};
-  g.out[2] = {up, f};
-  g.m = m; g.n = f; g.k[0] = d;
-  const bool fine = m <= kFineTokens;
-  P.fine = fine;
-  if ((st = ffn_gate_product(act, P, g, s)) != PRISM_OK) return st;
-  GemmProblem r;
-  r.a[0] = {h, f};
-  r.b[0] = {w->w_down, w->down_stride};
-  r.out[0] = {y, y_stride};
-  r.m = fine ? 2 * m : m;  // the values' rows, then the remainders': added to one another at the end
-  r.n = d; r.k[0] = f;
-  P.follows = 1;
-  P.fine = 0;
-  P.fold = fine ? int(m) : 0;
-  return ffn_product_nt(P, r, s);
+  return run_fwd(*w, m, act, x, x_stride, y, y_stride, gate, up, ws, reinterpret_cast<cudaStream_t>(stream), nullptr);
 }
 
 extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t m, int32_t act, prism_dtype dtype,
@@ -188,62 +261,26 @@ extern "C" prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t 
       if (p && cudaMemsetAsync(p, 0, size_t(d) * f * 2, s) != cudaSuccess) return PRISM_ERR_CUDA;
     return PRISM_OK;
   }
-  const size_t part = ffn_part_bytes(m, f);
-  const bool fine = m <= kFineTokens;
-  uint8_t* base = static_cast<uint8_t*>(ws) + kWsHeader;
-  void *dg = base, *du = base + part, *h = base + 2 * part;
-  GemmArgs P;
-  std::memset(&P, 0, sizeof(P));
-  P.status = ws_status(ws);
-  P.save = dw;
-  GemmProblem g;
-  g.a[0] = {dy, dy_stride};
-  g.in[0] = gate;
-  g.in[1] = up;
-  g.b[0] = {w->w_down, w->down_stride};
-  g.out[0] = {dg, f};
-  g.out[1] = {du, f};
-  g.out[2] = {h, f};
-  g.m = m; g.n = f; g.k[0] = d;
-  P.fine = fine;
-  if ((st = ffn_gate_bwd_product(act, P, g, s)) != PRISM_OK) return st;
-  P.follows = 1;
-  P.fine = 0;
-  if (dx) {
-    GemmProblem r;
-    r.a[0] = {dg, f};
-    r.a[1] = {du, f};
-    r.b[0] = {w->w_gate, w->gate_stride};
-    r.b[1] = {w->w_up, w->up_stride};
-    r.out[0] = {dx, dx_stride};
-    r.m = fine ? 2 * m : m;  // folded as in the forward
-    r.n = d; r.k[0] = f; r.k[1] = f;
-    P.fold = fine ? int(m) : 0;
-    if ((st = ffn_product_nn(P, r, s)) != PRISM_OK) return st;
-    P.fold = 0;
-  }
-  if (dw) {
-    GemmProblem r[3];
-    const void* a[3] = {dg, du, dy};
-    void* o[3] = {dw_gate, dw_up, dw_down};
-    for (int i = 0; i < 3; ++i) {
-      r[i].a[0] = {a[i], i < 2 ? f : dy_stride};
-      r[i].b[0] = {i < 2 ? x : h, i < 2 ? x_stride : f};
-      r[i].out[0] = {o[i], i < 2 ? d : f};
-      r[i].m = i < 2 ? f : d;
-      r[i].n = i < 2 ? d : f;
-      r[i].k[0] = m;
-      if (fine) {  // the remainders as a second segment of K
-        const int64_t below = m * f;
-        r[i].a[1] = r[i].a[0];
-        r[i].b[1] = r[i].b[0];
-        GemmOperand& o2 = i < 2 ? r[i].a[1] : r[i].b[1];
-        o2.base = static_cast<const __nv_bfloat16*>(o2.base) + below;
-        r[i].k[1] = m;
-      }
-    }
-    P.beside = dx != nullptr;
-    if ((st = ffn_products_tn(P, r, 3, s)) != PRISM_OK) return st;
+  return run_bwd(*w, m, act, dy, dy_stride, x, x_stride, gate, up, dx, dx_stride, dw_gate, dw_up, dw_down, ws, s, nullptr);
+}
+
+extern "C" prism_status prism_gated_ffn_forms(const prism_ffn_weights* w, int64_t m, int32_t backward, int32_t* forms) {
+  if (!w || !forms) return PRISM_ERR_ARG;
+  const prism_status st = check_ffn(m, w->d, w->f, PRISM_ACT_SILU, PRISM_BF16);
+  if (st != PRISM_OK) return st;
+  std::memset(forms, 0, sizeof(int32_t) * 9);
+  if (m == 0) return PRISM_OK;
+  GemmChoice c[3] = {};
+  alignas(16) char any[1];  // marks outputs that are wanted; nothing is launched
+  const int64_t d = w->d;
+  if (backward)
+    run_bwd(*w, m, PRISM_ACT_SILU, any, d, any, d, any, any, any, d, any, any, any, any, nullptr, c);
+  else
+    run_fwd(*w, m, PRISM_ACT_SILU, any, d, any, d, any, any, any, nullptr, c);
+  for (int i = 0; i < 3; ++i) {
+    forms[3 * i] = c[i].cg;
+    forms[3 * i + 1] = c[i].bn;
+    forms[3 * i + 2] = c[i].parts;
   }
   return PRISM_OK;
 }

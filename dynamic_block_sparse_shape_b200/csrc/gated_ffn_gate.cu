@@ -2,12 +2,12 @@
 #include "gated_ffn.h"
 
 namespace prism {
-prism_status ffn_gate_product(int act, GemmArgs& P, const GemmProblem& pr, cudaStream_t s) {
+prism_status ffn_gate_product(int act, GemmArgs& P, const GemmProblem& pr, cudaStream_t s, GemmChoice* form) {
   switch (act) {
-    case PRISM_ACT_SILU: return gemm<false, false, kEpiGate, PRISM_ACT_SILU>(P, &pr, 1, s);
-    case PRISM_ACT_GELU: return gemm<false, false, kEpiGate, PRISM_ACT_GELU>(P, &pr, 1, s);
-    case PRISM_ACT_GELU_TANH: return gemm<false, false, kEpiGate, PRISM_ACT_GELU_TANH>(P, &pr, 1, s);
+    case PRISM_ACT_SILU: return gemm<false, false, kEpiGate, PRISM_ACT_SILU>(P, &pr, 1, s, form);
+    case PRISM_ACT_GELU: return gemm<false, false, kEpiGate, PRISM_ACT_GELU>(P, &pr, 1, s, form);
+    case PRISM_ACT_GELU_TANH: return gemm<false, false, kEpiGate, PRISM_ACT_GELU_TANH>(P, &pr, 1, s, form);
   }
-  return gemm<false, false, kEpiGate, PRISM_ACT_RELU>(P, &pr, 1, s);
+  return gemm<false, false, kEpiGate, PRISM_ACT_RELU>(P, &pr, 1, s, form);
 }
 }  // namespace prism

@@ -264,8 +264,9 @@ inline GemmChoice gemm_choice(const int64_t* m, const int64_t* n, int products, 
   return c;
 }
 
+// `form`: only says which kernel and tiles it would take.
 template <bool AMN, bool BMN, int EPI, int ACT>
-prism_status gemm(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s) {
+prism_status gemm(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t s, GemmChoice* form) {
   // the gradient of the gate has the longest epilogue: it alternates its accumulators to hide it
   constexpr int kSub = EPI == kEpiGateBwd ? 1 : 2;
   int64_t m[kGemmProducts], n[kGemmProducts], slices = 0;
@@ -277,6 +278,10 @@ prism_status gemm(GemmArgs& P, const GemmProblem* pr, int products, cudaStream_t
     ragged = ragged || pr[i].a[0].ld % 64 || pr[i].b[0].ld % 64;
   }
   const GemmChoice c = gemm_choice(m, n, products, slices, AMN, kSub, ragged, P.fine || P.fold);
+  if (form) {
+    *form = c;
+    return PRISM_OK;
+  }
   if (c.bn == 0) return gemm_launch<kSub, AMN, BMN, EPI, ACT>(P, pr, products, s);
   if (c.cg == 1 && c.bn == 64) return gemm_split_launch<1, 64, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);
   if (c.cg == 1) return gemm_split_launch<1, 128, AMN, BMN, EPI, ACT>(P, pr, products, c.parts, s);

@@ -607,6 +607,15 @@ PRISM_API prism_status prism_gated_ffn_bwd(const prism_ffn_weights* w, int64_t m
                                            void* dw_gate, void* dw_up, void* dw_down, void* ws, size_t ws_bytes,
                                            void* stream);
 
+/* Host only, for tests and tuning: the kernel of each product of such a call of
+ * m tokens with contiguous rows. forms: host int32[9] out, three values each
+ * for the gate and the down product (backward 0), or for the gradient of the
+ * gate, dx and the weight gradients (1): CTAs that share a tile (1, or a pair),
+ * its accumulator's columns (0: the persistent kernel of pairs) and the parts
+ * of K that a cluster splits it into; all 0: no such product, or the kernel of
+ * a handful of tokens. */
+PRISM_API prism_status prism_gated_ffn_forms(const prism_ffn_weights* w, int64_t m, int32_t backward, int32_t* forms);
+
 /* Workspace bytes of prism_gated_ffn_fwd (backward 0) and _bwd (1). Host only. */
 PRISM_API prism_status prism_gated_ffn_workspace_size(int64_t m, int32_t f, int32_t backward, size_t* bytes);
 

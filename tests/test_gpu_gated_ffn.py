@@ -394,3 +394,59 @@ def test_far_projections(m, act):
     want = 2.0 ** -4 * 0.5 * slope
     tol = (2.0 ** -19 * (1 + 9.0) + 2 * STEP * (1 + STEP)) * np.maximum(np.abs(want), 2.0 ** -6) + 2.0 ** -120
     assert (np.abs(f64(dx) - want) <= tol).all()
+
+
+# with SIZES and LARGE, every kernel and split of K that a product can take: see test_every_form_is_reached
+FORMS = [(769, 8, 8), (17, 8, 328), (6194, 536, 8), (1973, 864, 8), (1142, 1968, 8), (17, 328, 2176), (1, 328, 9848),
+         (17, 2192, 1104), (41, 2392, 520), (26, 200, 9760), (29, 1008, 1096), (28, 856, 2408),
+         # pairs of CTAs with K in two parts: the last pair's second CTA with rows of its own, or wholly behind the last
+         (780, 1480, 728), (413, 1464, 1216), (643, 1552, 1704), (793, 1408, 1648)]
+PRODUCTS = ("gate", "down", "gradient of the gate", "dx", "weight gradients")
+
+
+def forms(m, d, f):
+    """The kernel of each product of a block: CTAs that share a tile, its columns (0: persistent), parts of K; whether
+    remainders come along; and of split pairs whether the last one's second CTA has rows."""
+    w, a, b = P._FfnWeights(0, 0, 0, d, d, f, d, f), (ctypes.c_int32 * 9)(), (ctypes.c_int32 * 9)()
+    assert P.lib().prism_gated_ffn_forms(ctypes.byref(w), m, 0, a) == 0
+    assert P.lib().prism_gated_ffn_forms(ctypes.byref(w), m, 1, b) == 0
+    found = set()
+    for name, c in zip(PRODUCTS, (tuple(x) for x in (a[0:3], a[3:6], b[0:3], b[3:6], b[6:9]))):
+        found.add((name, c, m <= 32, 1 <= m % 256 <= 128 if c[:2] == (2, 256) and name != PRODUCTS[4] else None))
+    return found
+
+
+def test_every_form_is_reached():
+    """The sizes of this file take every kernel that the choice takes over a wide range, so that a change of the choice
+    leaves none of them untested."""
+    from dynamic_block_sparse_shape_b200 import build
+    build.build()
+    reached = set().union(*(forms(*s) for s in SIZES + LARGE + FORMS))
+    r = np.random.default_rng(0)
+    many = np.exp(r.uniform(np.log([1, 1, 1]), np.log([16384, 512, 1408]), (20000, 3))).round().astype(int)
+    missing = {}
+    for m, d, f in many:
+        for k in forms(int(m), 8 * int(d), 8 * int(f)) - reached:
+            missing.setdefault(k, (m, 8 * d, 8 * f))
+    assert not missing
+    split = {n for n, c, _, _ in reached if c == (2, 256, 2)}
+    assert split == set(PRODUCTS)  # pairs that split K, in every product
+    w, a = P._FfnWeights(0, 0, 0, 8, 8, 8, 8, 8), (ctypes.c_int32 * 9)()
+    call = P.lib().prism_gated_ffn_forms
+    assert call(None, 1, 0, a) == 1 and call(ctypes.byref(w), 1, 0, None) == 1 and call(ctypes.byref(w), -1, 0, a) == 1
+    a[0] = 7
+    assert call(ctypes.byref(w), 0, 1, a) == 0 and list(a) == [0] * 9
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,d,f", FORMS)
+def test_every_form(m, d, f):
+    require_gpu()
+    act = ACTS[FORMS.index((m, d, f)) % len(ACTS)]
+    x, wg, wu, wd, dy = draw(m, d, f, m + d)
+    ws = P.Workspace("cuda")
+    y, g, u = P.gated_ffn_fwd(x, wg, wu, wd, act=act, ws=ws)
+    got = P.gated_ffn_bwd(dy, x, wg, wu, wd, g, u, act=act, ws=ws)
+    P.check_device_status(ws)
+    check_fwd(x, wg, wu, wd, act, y, g, u)
+    check_bwd(dy, x, wg, wu, wd, g, u, act, got)
