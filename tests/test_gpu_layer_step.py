@@ -143,3 +143,67 @@ def test_sharded_clipping():
         want = whole[:, slice(*head_shard(5, 2, r))]
         # factors 40 * 2^-24 apart round to neighbouring bf16 values at most
         assert ((p.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs()).all()
+
+
+@pytest.mark.gpu
+def test_step_after_other_sizes():
+    """The same bits again after other sizes, smaller and larger, used the shared workspace in between and let it grow."""
+    require_gpu()
+    x, weights = _inputs()
+    spec = P.RopeSpec((22, 20, 22), layout="half")
+    geo = P.Geometry(GRID, ZONE, ((4, 4, 4),))
+    ws = P.Workspace("cuda", 256)
+    first = _step(x, weights, spec, geo, ws)
+    b = lambda *s: torch.full(s, 0.5, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    for m, c, f in ((3, 64, 128), (3000, 264, 1032), (40, 2312, 72)):
+        y, gate, up = P.gated_ffn_fwd(b(m, c), b(f, c), b(f, c), b(c, f), ws=ws)
+        P.gated_ffn_bwd(y, b(m, c), b(f, c), b(f, c), b(c, f), gate, up, ws=ws)
+    P.clip_grad_norm([b(n) for n in range(1, 2000)], 1.0, ws=ws)
+    again = _step(x, weights, spec, geo, ws)
+    P.check_device_status(ws)
+    assert torch.equal(first["y"], again["y"]) and torch.equal(first["norm"], again["norm"])
+    for name in first["grads"]:
+        assert torch.equal(first["grads"][name], again["grads"][name]), name
+
+
+@pytest.mark.gpu
+def test_step_as_replayed_graphs():
+    """What lies before and behind the selection (which hands its total to the host) as two captured graphs that share a
+    workspace: replayed with other inputs they give an eager step's bits."""
+    require_gpu()
+    x, weights = _inputs()
+    spec = P.RopeSpec((22, 20, 22), layout="half")
+    geo = P.Geometry(GRID, ZONE, ((4, 4, 4),))
+    ws, sc, n = P.Workspace("cuda"), 1.0 / math.sqrt(D), x["q"].shape[0]
+    first = _step(x, weights, spec, geo, ws)  # grows the workspace, loads the kernels
+    sel = first["sel"]
+    torch.cuda.synchronize()
+    before, behind = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(before):
+        q, k = P.rope(x["q"], x["k"], spec, grid=GRID)
+        zs, _ = P.zone_shapes(geo, ws=ws)
+        qp, kp = P.block_pool(geo, zs, q, k, ws=ws)
+    with torch.cuda.graph(behind):
+        o_lo = torch.empty_like(q)
+        o, lse = P.bsa_fwd(geo, zs, q, k, x["v"], sc, sel["row_ptr"], sel["col_idx"], ws=ws, o_lo=o_lo)
+        h = o.reshape(n, HEADS * D)
+        y, gate, up = P.gated_ffn_fwd(h, *weights, act="gelu_tanh", ws=ws)
+        dh, dwg, dwu, dwd = P.gated_ffn_bwd(x["dy"], h, *weights, gate, up, act="gelu_tanh", ws=ws)
+        dqr, dkr, dv = P.bsa_bwd(geo, zs, q, k, x["v"], o, lse, dh.view(n, HEADS, D), sc, sel["row_ptr"], sel["col_idx"],
+                                 sel["total"], ws=ws, o_lo=o_lo)
+        dq, dk = P.rope_bwd(dqr, dkr, spec, grid=GRID)
+        grads = dict(dq=dq, dk=dk, dv=dv, dwg=dwg, dwu=dwu, dwd=dwd)
+        norm = P.clip_grad_norm(list(grads.values()), 0.5, ws=ws)
+    for scale in (1.0, -0.5):  # q and k, and so the selection, stay
+        x["v"].mul_(scale)
+        x["dy"].mul_(scale)
+        want = _step(x, weights, spec, geo, P.Workspace("cuda"))
+        before.replay()
+        again = P.block_select(qp, kp, sc, 2, 0.5, ws=ws)
+        assert torch.equal(again["col_idx"], sel["col_idx"]) and torch.equal(again["row_ptr"], sel["row_ptr"])
+        behind.replay()
+        torch.cuda.synchronize()
+        P.check_device_status(ws)
+        assert torch.equal(y, want["y"]) and torch.equal(norm, want["norm"])
+        for name in grads:
+            assert torch.equal(grads[name], want["grads"][name]), (name, scale)
