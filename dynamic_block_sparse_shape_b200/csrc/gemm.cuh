@@ -398,20 +398,23 @@ __device__ __forceinline__ void copy16(const uint32_t* from, uint32_t* to) {
 
 // kEpiGateBwd: the outputs of one 32-row, 32-column piece from dh in tensor
 // memory at `acc` and the saved projections' piece at `in` (gate, then up);
-// `taken` once that is read.
+// `taken` once that is read, which lets the next piece be copied over it. That
+// comes behind the first output's store, not behind the loads: a warp goes on
+// while its loads of shared memory still queue (behind the load of tensor memory),
+// and a copy need not wait for them. The first output holds every value of the
+// piece, so that its stores are issued shows that all loads are back; the fence in
+// there orders them against the copy.
 template <int ACT, typename F>
 __device__ __forceinline__ void gemm_piece_bwd(const GemmArgs& P, const GemmProduct& Q, uint32_t acc, PieceRing<32>& ring,
                                                const uint8_t* in, int lane, int row, int col, const F& taken) {
   uint32_t r[32], w[16], wg[16], wu[16];
-  tmem_ld32(acc, r);
   uint4 gv[4], uv[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     gv[c] = *reinterpret_cast<const uint4*>(in + Piece<32>::offset(lane, c));
     uv[c] = *reinterpret_cast<const uint4*>(in + Piece<32>::kBytes + Piece<32>::offset(lane, c));
   }
-  __syncwarp();
-  taken();
+  tmem_ld32(acc, r);
   tmem_ld_wait();
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -433,6 +436,7 @@ __device__ __forceinline__ void gemm_piece_bwd(const GemmArgs& P, const GemmProd
     w[i] = pack_bf16x2(h[0], h[1]);
   }
   ring.store(&Q.out[0], lane, row, col, [&](int, uint32_t* x) { copy16(wg, x); });
+  taken();
   ring.store(&Q.out[1], lane, row, col, [&](int, uint32_t* x) { copy16(wu, x); });
   if (P.save) ring.store(&Q.out[2], lane, row, col, [&](int, uint32_t* x) { copy16(w, x); });
 }

@@ -450,3 +450,27 @@ def test_every_form(m, d, f):
     P.check_device_status(ws)
     check_fwd(x, wg, wu, wd, act, y, g, u)
     check_bwd(dy, x, wg, wu, wd, g, u, act, got)
+
+
+@pytest.mark.gpu
+def test_wide_backward_repeats_itself():
+    """The same bits from several hundred calls. A copy of the saved projections of the epilogue's next piece that did not
+    wait for the reads of the last one changed a few rows of one call in fifty here."""
+    require_gpu()
+    m, d, f = 8192, 4096, 11264
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    dy, gate, up, wg, wu, wd = n(m, d), n(m, f), n(m, f), n(f, d), n(f, d), n(d, f)
+    ws = P.Workspace("cuda")
+
+    def call(need_dw=False):
+        return P.gated_ffn_bwd(dy, dy, wg, wu, wd, gate, up, need_dw=need_dw, ws=ws)
+
+    dx, *dw = call(True)
+    off = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(400):
+        off += (call()[0] != dx).sum()
+    for _ in range(50):
+        off += sum((a != b).sum() for a, b in zip(call(True), (dx, *dw)))
+    P.check_device_status(ws)
+    assert int(off) == 0
