@@ -95,6 +95,7 @@ _SIGNATURES = {
     "prism_workspace_size": (ctypes.c_int, [ctypes.c_int, _GEO, _I32, _I32, _I32, _I32, ctypes.c_int, _I64,
                                             ctypes.POINTER(_SZ)]),
     "prism_check_device_status": (ctypes.c_int, [_P, _P]),
+    "prism_clear_device_status": (ctypes.c_int, [_P, _P]),
     "prism_keep_device_status": (ctypes.c_int, [_P, _P]),
     "prism_check_kept_status": (ctypes.c_int, [_P, _P]),
     "prism_zone_shapes": (ctypes.c_int, [_GEO, _P, _I64, _I32, ctypes.c_int, _P, _I64, _I32, ctypes.c_int,
@@ -238,24 +239,29 @@ class Workspace:
     def ensure(self, nbytes: int):
         """Makes room for `nbytes`, for work on the current stream."""
         nbytes = max(int(nbytes), 256)
-        if self.device.index is not None and self.device.index != torch._C._cuda_getDevice():
+        if self.device.type == "cuda" and self.device.index not in (None, torch._C._cuda_getDevice()):
             with torch.cuda.device(self.device):
                 return self._ensure(nbytes)
         return self._ensure(nbytes)
 
     def _ensure(self, nbytes: int):
-        if self.buf is None or self.buf.numel() < nbytes + 256:
+        if self.buf is None or self.nbytes < nbytes:
             if self.captured:
                 self.kept.append(self.buf)
             self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
             self.start = (self.buf.data_ptr() + 255) // 256 * 256
-            at = self.start - self.buf.data_ptr()
-            self.buf[at:at + 256].zero_()  # the status word: every call writes the rest before it reads it
+            self.nbytes = nbytes
             self.captured = False
-            self.device = self.buf.device
-            self.home = _raw_stream(self.device.index) if self.buf.is_cuda else None
-        if self.buf.is_cuda:
-            if _raw_stream(self.device.index) != self.home:
+            self.device, self.index = self.buf.device, self.buf.get_device()
+            # the status word; every call writes the rest before it reads it
+            if self.index >= 0:
+                self.home = _raw_stream(self.index)
+                _check(lib().prism_clear_device_status(self.start, self.home), "workspace")
+            else:
+                at = self.start - self.buf.data_ptr()
+                self.buf[at:at + 256].zero_()
+        if self.index >= 0:
+            if _raw_stream(self.index) != self.home:
                 self.buf.record_stream(torch.cuda.current_stream(self.device))
             if torch.cuda.is_current_stream_capturing():
                 self.captured = True
@@ -265,13 +271,8 @@ class Workspace:
     def ptr(self):
         return ctypes.c_void_p(self.start)
 
-    @property
-    def nbytes(self):
-        return self.buf.numel() - (self.start - self.buf.data_ptr())
 
-
-def _raw_stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device's current stream
 
 
 def _require(ok: bool, what: str, status: int = 1):
@@ -328,9 +329,9 @@ class _On:
         if ws is None:
             self.passing = Workspace(torch.device("cuda", self.device), nbytes)
             return self.passing
-        if ws.buf.get_device() != self.device:
+        if ws.index != self.device:
             _require(False, what + ": a workspace of another device", 4)
-        return ws.ensure(nbytes)
+        return ws._ensure(nbytes)
 
 
 def check_device_status(ws: Optional[Workspace] = None, stream=None):

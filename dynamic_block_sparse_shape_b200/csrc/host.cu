@@ -166,6 +166,11 @@ __global__ void take_status_kernel(int* out) { *out = atomicExch(&g_kept_status,
 }  // namespace
 }  // namespace prism
 
+extern "C" prism_status prism_clear_device_status(void* ws, void* stream) {
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256) return PRISM_ERR_WORKSPACE;
+  return cuda_status(cudaMemsetAsync(ws, 0, kWsHeader, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 extern "C" prism_status prism_keep_device_status(const void* ws, void* stream) {
   if (!ws) return PRISM_ERR_WORKSPACE;
   keep_status_kernel<<<1, 1, 0, reinterpret_cast<cudaStream_t>(stream)>>>(static_cast<const int*>(ws));

@@ -41,8 +41,8 @@
  *   library never allocates or frees device memory: scratch comes from the
  *   caller's workspace `ws` of `ws_bytes` bytes (256-byte aligned), sized by
  *   prism_workspace_size(). Its first 256 bytes, the device status word, have
- *   to be zero before the first call that uses it (cleared in the order of that
- *   call's stream); the rest needs no value. Work is enqueued on `stream` (a
+ *   to be zero before the first call that uses it (prism_clear_device_status on
+ *   that call's stream); the rest needs no value. Work is enqueued on `stream` (a
  *   cudaStream_t; NULL is the legacy default stream) and is asynchronous unless
  *   stated.
  * - Every call validates its arguments on the host and returns a status; no
@@ -130,6 +130,9 @@ PRISM_API prism_status prism_geometry_counts(const prism_geometry* geo, int32_t*
 PRISM_API prism_status prism_workspace_size(prism_op op, const prism_geometry* geo, int32_t heads, int32_t head_dim,
                                   int32_t feat_c, int32_t res_c, prism_dtype in_dtype, int64_t nnz,
                                   size_t* bytes);
+
+/* Clears the first 256 bytes of `ws`, in the order of `stream`. */
+PRISM_API prism_status prism_clear_device_status(void* ws, void* stream);
 
 /* Reads and clears the device status word kept in `ws` (synchronises
  * `stream`). Returns PRISM_ERR_TIMEOUT or PRISM_ERR_DEVICE if a kernel that

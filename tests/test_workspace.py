@@ -54,6 +54,8 @@ def test_refusals_of_kept_status():
     """Host checks of the status calls, before any CUDA call."""
     from dynamic_block_sparse_shape_b200 import build
     build.build()
+    assert P.lib().prism_clear_device_status(None, None) == 4
+    assert P.lib().prism_clear_device_status(8, None) == 4
     assert P.lib().prism_keep_device_status(None, None) == 4
     assert P.lib().prism_check_kept_status(None, None) == 4
     assert P.lib().prism_check_kept_status(8, None) == 4
