@@ -22,8 +22,8 @@
 // Measured, 16384 x 4096 x 11264 with the power cap reached (the library's bf16
 // product alone: 1439 TFLOP/s of 8192^3, 1322 to 1390 of these shapes): gate 1291
 // TFLOP/s, down 1411, dx 1430, weight gradients 1418, the tensor pipe 88 to 95 %
-// busy; gradient of the gate 1029 (70 %), whose epilogue reads two and writes three
-// [M, F] tensors beside the products.
+// busy; gradient of the gate 1029 (70 %), whose SUB = 1 tiles and epilogue pieces (two
+// [M, F] tensors read, three written) want 64 + 10 bytes per cycle and SM.
 //
 // Roles of a CTA's ten warps: 0 issues the copies into a ring of slices; 1
 // owns the tensor memory and issues the products (of the pair: the leader's);

@@ -31,7 +31,8 @@
 // there in place by narrower vectors, and back in 16-byte vectors.
 //
 // With one or two heads the angles are most of the work and the kernel is bound
-// by instructions (2.6 times the floor for one head each of Q and K, 101 pairs);
+// by instructions (2.6 times the floor for one head each of Q and K, 101 pairs; on a
+// grid the angles of t and h are formed for each token, though its neighbours' are alike);
 // the hardware's approximate sine and cosine would take 8 % off that and lose
 // three bits, so the exact ones stay.
 #include <cuda_bf16.h>
