@@ -293,11 +293,12 @@ class _On:
                 _require(False, what + ": tensors on different devices")
         if index < 0:
             _require(False, what + ": tensors must be on a CUDA device")
+        if stream is not None and stream.device_index != index:
+            _require(False, what + ": a stream of another device")
         self.device = index
         self.guard = self.caller = self.passing = None
         self.ptr = _raw_stream(index)
         if stream is not None and stream.cuda_stream != self.ptr:
-            _require(stream.device_index == index, what + ": a stream of another device")
             self.caller = torch.cuda.current_stream(index)
             self.ptr = stream.cuda_stream
             self.guard = torch.cuda.stream(stream)

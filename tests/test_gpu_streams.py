@@ -151,3 +151,70 @@ def test_memory_stays_with_the_streams_that_use_it():
     assert all(not t.data_ptr() <= held < t.data_ptr() + t.numel() for t in again)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_forked_inside_a_capture():
+    """A call on a side stream that joins the captured one: with a workspace, and without one."""
+    require_gpu()
+    x, wg, wu, wd, dy = ffn(300, 1160, 392)
+    grads = [torch.ones(n, device="cuda") for n in (1000, 300000)]
+    ws = P.Workspace("cuda")
+    want = P.gated_ffn_fwd(x, wg, wu, wd, ws=ws)
+    wantb = P.gated_ffn_bwd(dy, x, wg, wu, wd, want[1], want[2], ws=ws)
+    norm = P.grad_norm(grads)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = P.gated_ffn_fwd(x, wg, wu, wd, stream=side)
+        gotb = P.gated_ffn_bwd(dy, x, wg, wu, wd, got[1], got[2], ws=ws, stream=side)
+        n = P.grad_norm(grads, stream=side)
+        here.wait_stream(side)
+        y2 = got[0] + 0
+    junk = [torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for _ in range(3):
+        for t in (*got, *gotb, n, y2):
+            t.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*got, *gotb, n, y2), (*want, *wantb, norm, want[0])))
+    assert all((j == 255).all() for j in junk)
+    P.check_device_status(ws)
+    P.check_device_status()
+
+
+def test_two_threads_at_once():
+    """Calls from several host threads, each on a stream and with memory of its own."""
+    require_gpu()
+    import threading
+    sizes = [(1, 256, 512), (33, 256, 512), (300, 1160, 392), (900, 520, 264)]
+    data = [ffn(*s) for s in sizes]
+    spec = P.RopeSpec((44, 42, 42))
+    q = torch.randn((360, 4, 128), device="cuda")
+
+    def work(x, wg, wu, wd, dy, s):
+        y, g, u = P.gated_ffn_fwd(x, wg, wu, wd, stream=s)
+        r = [y, g, u, *P.gated_ffn_bwd(dy, x, wg, wu, wd, g, u, stream=s), P.rope(q, None, spec, grid=(4, 9, 10), stream=s)[0]]
+        return r + [P.grad_norm([y, g, u], stream=s)]
+
+    want = [work(*d, None) for d in data]
+    torch.cuda.synchronize()
+    off = []
+
+    def run(i):
+        s = torch.cuda.Stream()
+        for _ in range(40):
+            got = work(*data[i], s)
+            s.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                off.append(i)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(data))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not off
+    P.check_device_status()

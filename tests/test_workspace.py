@@ -1,4 +1,6 @@
 """The binding's workspaces and streams, as far as that goes without a GPU."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -48,6 +50,13 @@ def test_a_workspace_of_another_device_is_refused():
     with pytest.raises(P.PrismError) as e:
         call.workspace(P.Workspace("cpu"), 1024, "a call")
     assert e.value.status == 4
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Also when both are the default stream, whose handle is the same on every device."""
+    tensor, stream = SimpleNamespace(get_device=lambda: 0), SimpleNamespace(device_index=1, cuda_stream=0)
+    with pytest.raises(P.PrismError, match="another device"):
+        P._On([tensor], stream, "a call")
 
 
 def test_refusals_of_kept_status():
